@@ -101,7 +101,7 @@ def fused_linear(desc, blob, shape, x, codec: str, out=None, stream=None, status
     rows, cols = int(shape[0]), int(shape[1])
     if x.dim() != 2 or x.shape[1] != cols or x.dtype != torch.bfloat16:
         raise ValueError(f"x must be M x {cols} BF16")
-    x = x.contiguous()
+    x = _contiguous_on(x, stream)
     M = int(x.shape[0])
     if out is None:
         out = torch.empty((M, rows), dtype=torch.float32, device=x.device)
@@ -200,6 +200,14 @@ class _On:
     def __exit__(self, *error):
         if self.stack is not None:
             return self.stack.__exit__(*error)
+
+
+def _contiguous_on(x, stream):
+    """x with adjacent elements; a copy is made, and belongs, where it is read: on ``stream``."""
+    if x.is_contiguous():
+        return x
+    with _On(x.device, stream, (x,)):
+        return x.contiguous()
 
 
 def _workspace(nbytes, device):
@@ -544,13 +552,14 @@ class TiledWeights:
         rows, cols = self.shapes[index]
         if x.dim() != 2 or x.shape[1] != cols or x.dtype != torch.bfloat16:
             raise ValueError(f"x must be M x {cols} BF16")
-        return rows, cols, x.contiguous()
+        return rows, cols
 
     def gemm(self, index: int, x, out=None, stream=None, status=None):
         """y = x W^T for matrix ``index``; x: M x cols BF16 (M <= 256). Returns
         ``out`` (M x rows FP32, allocated if None)."""
         import torch
-        rows, cols, x = self._check_x(index, x)
+        rows, cols = self._check_x(index, x)
+        x = _contiguous_on(x, stream)
         M = int(x.shape[0])
         if out is None:
             out = torch.empty((M, rows), dtype=torch.float32, device=x.device)
@@ -561,7 +570,10 @@ class TiledWeights:
     def gemm_batched(self, indices, xs, outs=None, stream=None, status=None):
         """Several matrices (at most 8), one launch; all x share M."""
         import torch
-        xs = [self._check_x(i, x)[2] for i, x in zip(indices, xs)]
+        pairs = list(zip(indices, xs))
+        for i, x in pairs:
+            self._check_x(i, x)
+        xs = [_contiguous_on(x, stream) for _, x in pairs]
         M = int(xs[0].shape[0])
         if any(int(x.shape[0]) != M for x in xs):
             raise ValueError("all activations of a batched call share M")
@@ -582,9 +594,13 @@ class TiledWeights:
         act_id = _act_id(act)
         if self.shapes[gate] != self.shapes[up]:
             raise ValueError(f"matrices differ in shape: {self.shapes[gate]}, {self.shapes[up]}")
-        rows, _, x = self._check_x(gate, x)
+        rows, _ = self._check_x(gate, x)
         M = int(x.shape[0])
         with _On(x.device, stream, (x,)) as s:
+            # laid out on the stream that reads it
+            x = x.contiguous()
+            if x.data_ptr() % 16:
+                x = x.clone()
             if out is None:
                 out = torch.empty((M, rows), dtype=torch.bfloat16, device=x.device)
             else:

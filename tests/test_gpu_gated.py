@@ -472,3 +472,27 @@ def test_tiled_weights(codec, M):
     for act in ACTS:
         e = Exact(act, x, wg, wu)
         close(tw.gated(gate, up, x, act=act), e.h, e.h_tol)
+
+
+def test_tiled_weights_on_another_stream():
+    """An x that has to be laid out first, on a stream of its own while the current one is busy: the copy is
+    made where it is read (unaligned rows too)."""
+    N, K, M = 256, 192, 40
+    wg, wu = (synth.normal_bf16((N, K), seed=s, sigma=0.05, outlier_frac=1e-3, device="cuda") for s in (3, 4))
+    tw = layers.TiledWeights("cuda")
+    gate, up = tw.add(wg), tw.add(wu)
+    x = torch.randn(M, K, generator=torch.Generator("cuda").manual_seed(20), device="cuda").bfloat16()
+    want, a = tw.gated(gate, up, x), tw.gemm(gate, x)
+    odd = torch.zeros(M * K + 1, dtype=x.dtype, device="cuda")
+    odd[1:] = x.view(-1)
+    side = torch.cuda.Stream()
+    strided, odd = x.t().contiguous().t(), odd[1:].view(M, K)
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(20_000_000)   # some 10 ms on the current stream
+        got = [tw.gated(gate, up, strided, stream=stream), tw.gated(gate, up, odd, stream=stream)]
+        b = tw.gemm(gate, strided, stream=stream)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            assert all(torch.equal(g, want) for g in got) and torch.equal(a, b)
+        torch.cuda.synchronize()

@@ -1,0 +1,69 @@
+"""Which stream the operators' own copies run on, and which tensors they record
+there, checked with the library's calls replaced by recorders (no GPU needed)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from decode_dfloat11_b200 import layers, lwc  # noqa: E402
+
+STREAM = "another stream"
+
+
+class Recorder:
+    """Stands for layers._On: where one is inside it, and what it was given."""
+    inside = []
+    given = []
+
+    def __init__(self, device, stream=None, used=()):
+        self.stream, self.used = stream, used
+
+    def __enter__(self):
+        Recorder.inside.append(self.stream)
+        Recorder.given.append((self.stream, self.used))
+        return self.stream
+
+    def __exit__(self, *error):
+        Recorder.inside.pop()
+
+
+@pytest.fixture
+def recorder(monkeypatch):
+    Recorder.inside, Recorder.given = [], []
+    monkeypatch.setattr(layers, "_On", Recorder)
+    copies = []
+    plain = torch.Tensor.contiguous
+
+    def contiguous(self, *args, **kwargs):
+        if not self.is_contiguous():
+            copies.append(list(Recorder.inside))
+        return plain(self, *args, **kwargs)
+
+    monkeypatch.setattr(torch.Tensor, "contiguous", contiguous)
+    Recorder.copies = copies
+    return Recorder
+
+
+@pytest.fixture
+def tiled(monkeypatch):
+    """TiledWeights of two 128 x 64 matrices, with calls that do nothing."""
+    for name in ("lwc_gemm_dfloat11", "lwc_gemm_dfloat11_batched", "lwc_gated_product", "lwc_linear_dfloat11"):
+        monkeypatch.setattr(lwc, name, lambda *args, **kwargs: None)
+    tw = layers.TiledWeights("cpu")
+    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc(), lwc.lwc_desc()], [None, None], [(128, 64), (128, 64)]
+    return tw
+
+
+@pytest.mark.parametrize("call", ["gated", "gemm", "gemm_batched", "fused_linear"])
+def test_a_strided_x_is_copied_on_the_stream_that_reads_it(recorder, tiled, call):
+    x = torch.zeros(64, 4, dtype=torch.bfloat16).t()
+    if call == "gated":
+        tiled.gated(0, 1, x, stream=STREAM)
+    elif call == "gemm":
+        tiled.gemm(0, x, stream=STREAM)
+    elif call == "gemm_batched":
+        tiled.gemm_batched([0, 1], [x, x], stream=STREAM)
+    else:
+        layers.fused_linear(lwc.lwc_desc(), None, (128, 64), x, "dfloat11", stream=STREAM, route="fused")
+    assert recorder.copies and all(STREAM in where for where in recorder.copies)
+    # and x itself is not given back before the copy was made
+    assert any(stream == STREAM and any(t is x for t in used) for stream, used in recorder.given)
