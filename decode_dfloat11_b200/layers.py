@@ -295,7 +295,7 @@ def gated_ffn(x, w_gate, w_up, act: str = "silu", out=None, stream=None, status=
     if (x.requires_grad or w_gate.requires_grad or w_up.requires_grad) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out cannot be given where gradients are needed")
-        with _On(x.device, stream):
+        with _On(x.device, stream, (x, w_gate, w_up)):
             return _functions()["gated"].apply(x, w_gate, w_up, act, status)
     if out is not None:
         _check_out(out, (*x.shape[:-1], w_gate.shape[0]), x)
@@ -372,8 +372,12 @@ def linear_cross_entropy_backward(grad, lse, x, w_head, targets, ignore_index: i
 
 
 def _check_xent(x, w_head, targets, reduction):
-    import torch
     _check_matrices(x, w_head=w_head)
+    _check_targets(x, targets, reduction)
+
+
+def _check_targets(x, targets, reduction):
+    import torch
     if reduction not in REDUCTIONS:
         raise ValueError(f"unknown reduction {reduction!r}")
     if targets.shape != x.shape[:-1] or targets.device != x.device or \
@@ -403,7 +407,7 @@ def linear_cross_entropy(x, w_head, targets, ignore_index: int = -100, reduction
     import torch
     _check_xent(x, w_head, targets, reduction)
     if (x.requires_grad or w_head.requires_grad) and torch.is_grad_enabled():
-        with _On(x.device, stream):
+        with _On(x.device, stream, (x, w_head, targets)):
             loss, lse = _functions()["xent"].apply(x, w_head, targets, ignore_index, reduction, status)
     else:
         loss, lse = _xent_forward(x, w_head, targets, ignore_index, reduction, stream, status)
@@ -797,7 +801,7 @@ class ResidentModel:
         if torch.is_grad_enabled() and x.requires_grad:
             if out is not None:
                 raise ValueError("out cannot be given where gradients are needed")
-            with _On(x.device, stream):
+            with _On(x.device, stream, (x,)):
                 return _functions()["resident_gated"].apply(x, self, layer, gate, up, act, status, route)
         if out is not None:
             _check_out(out, (*x.shape[:-1], rows), x)
@@ -812,8 +816,9 @@ class ResidentModel:
         import torch
         if x.device != self.layers[layer]["blobs"][index].device:
             raise ValueError("x must be on the matrix's device")
+        _check_targets(x, targets, reduction)
         if x.requires_grad and torch.is_grad_enabled():
-            with _On(x.device, stream):
+            with _On(x.device, stream, (x, targets)):
                 return _functions()["resident_xent"].apply(x, self, layer, index, targets, ignore_index, reduction,
                                                            status)
         with _On(x.device, stream, (x, targets,)) as s:

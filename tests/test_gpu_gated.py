@@ -496,3 +496,56 @@ def test_tiled_weights_on_another_stream():
         with torch.cuda.stream(side):
             assert all(torch.equal(g, want) for g in got) and torch.equal(a, b)
         torch.cuda.synchronize()
+
+
+def late(stream, call, *tensors):
+    """call(*copies of tensors) on `stream` behind some 10 ms of other work, where the copies are freed, and
+    their memory written again, long before the call's kernels run."""
+    copies = [t.clone().requires_grad_(t.requires_grad) for t in tensors]
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)
+    result = call(*copies).detach()
+    del copies
+    junk = [torch.full_like(t, 7) for t in tensors for _ in range(2)]
+    assert not stream.query(), "the work ahead of the call ended too early to show anything"
+    torch.cuda.synchronize()
+    return result, junk
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_operands_freed_before_the_stream_reads_them(grad):
+    x, wg, wu, _ = inputs(300, 512, 256, torch.bfloat16, seed=21)
+    t = torch.randint(0, 512, (300,), generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    wants = (layers.gated_ffn(x, wg, wu), layers.linear_cross_entropy(x, wg, t, reduction="none"))
+    x.requires_grad_(grad)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, _ = late(s, lambda x, wg, wu: layers.gated_ffn(x, wg, wu, stream=s), x, wg, wu)
+    assert torch.equal(got, wants[0])
+    got, _ = late(s, lambda x, w, t: layers.linear_cross_entropy(x, w, t, reduction="none", stream=s), x, wg, t)
+    assert torch.equal(got, wants[1])
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("codec", layers.CODECS)
+def test_operands_of_compressed_forms_freed_before_the_stream_reads_them(codec, grad):
+    N, K = 264, 320
+    wg, wu = (synth.normal_bf16((N, K), seed=s, sigma=0.05, outlier_frac=1e-3, device="cuda") for s in (1, 2))
+    model = resident(codec, wg, wu)
+    g = torch.Generator("cuda").manual_seed(2)
+    x = torch.randn(8, K, generator=g, device="cuda").bfloat16()
+    t = torch.randint(0, N, (8,), generator=g, device="cuda")
+    s = torch.cuda.Stream()
+    for route in ("decode", "fused"):
+        want = layers.gated_ffn(x, wg, wu)
+        x.requires_grad_(grad)
+        got, _ = late(s, lambda x: model.gated(0, 0, 1, x, stream=s, route=route), x)
+        x.requires_grad_(False)
+        e = Exact("silu", x, wg, wu)
+        close(got, e.h, e.h_tol)
+        assert route == "fused" or torch.equal(got, want)
+    want = model.cross_entropy(0, 0, x, t, reduction="none")
+    x.requires_grad_(grad)
+    got, _ = late(s, lambda x, t: model.cross_entropy(0, 0, x, t, reduction="none", stream=s), x, t)
+    assert torch.equal(got, want)

@@ -67,3 +67,35 @@ def test_a_strided_x_is_copied_on_the_stream_that_reads_it(recorder, tiled, call
     assert recorder.copies and all(STREAM in where for where in recorder.copies)
     # and x itself is not given back before the copy was made
     assert any(stream == STREAM and any(t is x for t in used) for stream, used in recorder.given)
+
+
+@pytest.mark.parametrize("call", ["gated_ffn", "linear_cross_entropy", "resident gated", "resident cross_entropy"])
+def test_differentiable_calls_record_what_they_read(recorder, monkeypatch, call):
+    """Their owner may free the operands (a loss dropped without a backward pass) before the stream read them."""
+    class Function:
+        @staticmethod
+        def apply(*args):
+            return torch.zeros(()), torch.zeros(())
+
+    monkeypatch.setattr(layers, "_functions", lambda: dict.fromkeys(("gated", "xent", "resident_gated", "resident_xent"),
+                                                                    Function))
+    monkeypatch.setattr(layers, "_check_matrices", lambda x, **matrices: None)
+    x = torch.zeros(2, 8, dtype=torch.bfloat16, requires_grad=True)
+    w, v = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(4, 8, dtype=torch.bfloat16)
+    t = torch.zeros(2, dtype=torch.int64)
+    model = layers.ResidentModel("codebook", "cpu")
+    model.layers.append(dict(descs=[lwc.lwc_desc()] * 2, blobs=[torch.zeros(1)] * 2, shapes=[(4, 8)] * 2))
+    if call == "gated_ffn":
+        read = [x, w, v]
+        layers.gated_ffn(x, w, v, stream=STREAM)
+    elif call == "linear_cross_entropy":
+        read = [x, w, t]
+        layers.linear_cross_entropy(x, w, t, stream=STREAM)
+    elif call == "resident gated":
+        read = [x]
+        model.gated(0, 0, 1, x, stream=STREAM)
+    else:
+        read = [x, t]
+        model.cross_entropy(0, 0, x, t, stream=STREAM)
+    used = [u for stream, given in recorder.given if stream == STREAM for u in given]
+    assert all(any(u is r for u in used) for r in read)
