@@ -175,7 +175,7 @@ def _rows(t):
 class _On:
     """Work on ``device`` and ``stream`` (None: the device's current stream),
     with allocations that belong to it; gives the raw stream. ``used``: tensors
-    that the work touches and that their owner may free before it ran."""
+    that the work reads or writes and that their owner may free before it ran."""
     __slots__ = ("device", "stream", "used", "stack")
 
     def __init__(self, device, stream=None, used=()):
@@ -194,7 +194,8 @@ class _On:
             return current.cuda_stream
         self.stack.enter_context(torch.cuda.stream(self.stream))
         for t in self.used:
-            t.record_stream(self.stream)
+            if hasattr(t, "record_stream"):   # a status word or an output may be None, or a plain address
+                t.record_stream(self.stream)
         return self.stream.cuda_stream
 
     def __exit__(self, *error):
@@ -238,7 +239,7 @@ def _check_gated(x, w_gate, w_up, act):
 
 def _gated_forward(x, w_gate, w_up, act, out, stream, status):
     N = w_gate.shape[0]
-    with _On(x.device, stream, (x, w_gate, w_up)) as s:
+    with _On(x.device, stream, (x, w_gate, w_up, out, status)) as s:
         if out is None:
             out = x.new_empty((*x.shape[:-1], N))
         g, keep = _gated_problem(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), w_gate, w_up, act)
@@ -248,7 +249,7 @@ def _gated_forward(x, w_gate, w_up, act, out, stream, status):
 
 def _gated_backward(dh, x, w_gate, w_up, act, need, stream, status):
     N = w_gate.shape[0]
-    with _On(x.device, stream, (dh, x, w_gate, w_up)) as s:
+    with _On(x.device, stream, (dh, x, w_gate, w_up, status)) as s:
         g, keep = _gated_problem(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), w_gate, w_up, act)
         dh2 = dh if dh.dim() == 2 else dh.reshape(-1, N)
         if not dh2.is_contiguous() and (N > 1 and dh2.stride(1) != 1 or dh2.shape[0] > 1 and dh2.stride(0) < N):
@@ -295,7 +296,7 @@ def gated_ffn(x, w_gate, w_up, act: str = "silu", out=None, stream=None, status=
     if (x.requires_grad or w_gate.requires_grad or w_up.requires_grad) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out cannot be given where gradients are needed")
-        with _On(x.device, stream, (x, w_gate, w_up)):
+        with _On(x.device, stream, (x, w_gate, w_up, status)):
             return _functions()["gated"].apply(x, w_gate, w_up, act, status)
     if out is not None:
         _check_out(out, (*x.shape[:-1], w_gate.shape[0]), x)
@@ -330,7 +331,7 @@ def _flat_targets(targets):
 def _xent_forward(x, head, targets, ignore_index, reduction, stream, status):
     """(the loss, reduced or per token, and the lse per token)."""
     import torch
-    with _On(x.device, stream, (x, head, targets)) as s:
+    with _On(x.device, stream, (x, head, targets, status)) as s:
         p, keep = _xent_problem(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), head, _flat_targets(targets),
                                 ignore_index)
         loss = torch.empty(targets.shape, dtype=torch.float32, device=x.device)
@@ -343,7 +344,7 @@ def _xent_forward(x, head, targets, ignore_index, reduction, stream, status):
 
 
 def _xent_backward(grad, lse, x, w_head, targets, ignore_index, reduction, need, stream, status):
-    with _On(x.device, stream, (grad, lse, x, w_head, targets)) as s:
+    with _On(x.device, stream, (grad, lse, x, w_head, targets, status)) as s:
         p, keep = _xent_problem(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), w_head, _flat_targets(targets),
                                 ignore_index)
         grad, lse = grad.contiguous(), lse.contiguous()
@@ -407,7 +408,7 @@ def linear_cross_entropy(x, w_head, targets, ignore_index: int = -100, reduction
     import torch
     _check_xent(x, w_head, targets, reduction)
     if (x.requires_grad or w_head.requires_grad) and torch.is_grad_enabled():
-        with _On(x.device, stream, (x, w_head, targets)):
+        with _On(x.device, stream, (x, w_head, targets, status)):
             loss, lse = _functions()["xent"].apply(x, w_head, targets, ignore_index, reduction, status)
     else:
         loss, lse = _xent_forward(x, w_head, targets, ignore_index, reduction, stream, status)
@@ -600,7 +601,7 @@ class TiledWeights:
             raise ValueError(f"matrices differ in shape: {self.shapes[gate]}, {self.shapes[up]}")
         rows, _ = self._check_x(gate, x)
         M = int(x.shape[0])
-        with _On(x.device, stream, (x,)) as s:
+        with _On(x.device, stream, (x, out, status)) as s:
             # laid out on the stream that reads it
             x = x.contiguous()
             if x.data_ptr() % 16:
@@ -758,7 +759,7 @@ class ResidentModel:
         M = x.numel() // cols
         if route == "auto":
             route = "fused" if x.dtype == torch.bfloat16 and 1 <= M <= _gated_fused_rows(self.codec, cols) else "decode"
-        with _On(x.device, stream, (x,)) as s:
+        with _On(x.device, stream, (x, out, status)) as s:
             if route == "decode":
                 w_gate, w_up = self._decoded(layer, (gate, up), s, status)
                 _check_matrices(x, w_gate=w_gate, w_up=w_up)
@@ -801,7 +802,7 @@ class ResidentModel:
         if torch.is_grad_enabled() and x.requires_grad:
             if out is not None:
                 raise ValueError("out cannot be given where gradients are needed")
-            with _On(x.device, stream, (x,)):
+            with _On(x.device, stream, (x, status)):
                 return _functions()["resident_gated"].apply(x, self, layer, gate, up, act, status, route)
         if out is not None:
             _check_out(out, (*x.shape[:-1], rows), x)
@@ -818,10 +819,10 @@ class ResidentModel:
             raise ValueError("x must be on the matrix's device")
         _check_targets(x, targets, reduction)
         if x.requires_grad and torch.is_grad_enabled():
-            with _On(x.device, stream, (x, targets)):
+            with _On(x.device, stream, (x, targets, status)):
                 return _functions()["resident_xent"].apply(x, self, layer, index, targets, ignore_index, reduction,
                                                            status)
-        with _On(x.device, stream, (x, targets,)) as s:
+        with _On(x.device, stream, (x, targets, status)) as s:
             (w,) = self._decoded(layer, (index,), s, status)
             return linear_cross_entropy(x, w, targets, ignore_index, reduction, status=status)
 

@@ -99,3 +99,36 @@ def test_differentiable_calls_record_what_they_read(recorder, monkeypatch, call)
         model.cross_entropy(0, 0, x, t, stream=STREAM)
     used = [u for stream, given in recorder.given if stream == STREAM for u in given]
     assert all(any(u is r for u in used) for r in read)
+
+
+@pytest.mark.parametrize("call", ["tiled gated", "gated_ffn", "resident gated", "gated_ffn_backward",
+                                  "linear_cross_entropy", "linear_cross_entropy_backward"])
+def test_outputs_and_status_words_are_recorded_too(recorder, tiled, monkeypatch, call):
+    """What the stream writes late must not be another tensor's memory by then."""
+    for name in ("lwc_gated_forward", "lwc_gated_backward", "lwc_xent_forward", "lwc_xent_backward",
+                 "lwc_linear_codebook_batched"):
+        monkeypatch.setattr(lwc, name, lambda *args, **kwargs: None)
+    for name in ("lwc_gated_backward_workspace_bytes", "lwc_xent_forward_workspace_bytes",
+                 "lwc_xent_backward_workspace_bytes"):
+        monkeypatch.setattr(lwc, name, lambda *args, **kwargs: 0)
+    monkeypatch.setattr(layers, "_check_matrices", lambda x, **matrices: None)
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(128, 64, dtype=torch.bfloat16)
+    t, f = torch.zeros(2, dtype=torch.int64), torch.zeros(2)
+    out, status = torch.zeros(2, 128, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    if call == "tiled gated":
+        tiled.gated(0, 1, x, out=out, stream=STREAM, status=status)
+    elif call == "gated_ffn":
+        layers.gated_ffn(x, w, w, out=out, stream=STREAM, status=status)
+    elif call == "resident gated":
+        model = layers.ResidentModel("codebook", "cpu")
+        model.layers.append(dict(descs=[lwc.lwc_desc()] * 2, blobs=[torch.zeros(1)] * 2, shapes=[(128, 64)] * 2))
+        model.gated(0, 0, 1, x, out=out, stream=STREAM, status=status)
+    elif call == "gated_ffn_backward":
+        layers.gated_ffn_backward(out, x, w, w, stream=STREAM, status=status)
+    elif call == "linear_cross_entropy":
+        layers.linear_cross_entropy(x, w, t, stream=STREAM, status=status)
+    else:
+        layers.linear_cross_entropy_backward(f, f, x, w, t, reduction="none", stream=STREAM, status=status)
+    used = [u for stream, given in recorder.given if stream == STREAM for u in given]
+    assert any(u is status for u in used)
+    assert any(u is out for u in used) or call.startswith("linear")
