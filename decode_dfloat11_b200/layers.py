@@ -594,9 +594,12 @@ class TiledWeights:
         """h = act(x W_gate^T) * (x W_up^T) for two matrices of one shape, held
         in tile order: both products in one launch (x: M x cols BF16, M <=
         256), then the activation and the product. Returns ``out`` (M x rows
-        BF16, allocated if None)."""
+        BF16, allocated if None). Not differentiable (``ResidentModel.gated``
+        is): an x that asks for a gradient is refused."""
         import torch
         act_id = _act_id(act)
+        if x.requires_grad and torch.is_grad_enabled():
+            raise ValueError("no gradient passes through TiledWeights.gated (give x.detach(), or use ResidentModel.gated)")
         if self.shapes[gate] != self.shapes[up]:
             raise ValueError(f"matrices differ in shape: {self.shapes[gate]}, {self.shapes[up]}")
         rows, _ = self._check_x(gate, x)

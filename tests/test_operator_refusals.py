@@ -1,5 +1,6 @@
 """Arguments that the gated block and the vocabulary cross entropy refuse,
 before any device work (no GPU needed), and what their Python forms check."""
+import contextlib
 import ctypes
 
 import pytest
@@ -145,3 +146,20 @@ def test_python_forms_check_their_arguments():
         layers.linear_cross_entropy(x.double(), w, t)
     with pytest.raises(ValueError, match="activation"):
         layers._act_id("swish2")
+
+
+def test_a_product_without_a_gradient_refuses_to_drop_one(monkeypatch):
+    """TiledWeights.gated has no backward pass: its result would silently end the graph."""
+    torch = pytest.importorskip("torch")
+    tw = layers.TiledWeights("cpu")
+    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc(), lwc.lwc_desc()], [None, None], [(128, 64), (128, 64)]
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(ValueError, match="gradient"):
+        tw.gated(0, 1, x)
+    # nothing is asked for: taken
+    for name in ("lwc_gemm_dfloat11_batched", "lwc_gated_product"):
+        monkeypatch.setattr(lwc, name, lambda *args, **kwargs: None)
+    monkeypatch.setattr(layers, "_On", lambda *args: contextlib.nullcontext())
+    with torch.no_grad():
+        assert tw.gated(0, 1, x).shape == (2, 128)
+    assert tw.gated(0, 1, x.detach()).shape == (2, 128)
