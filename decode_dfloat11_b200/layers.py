@@ -619,6 +619,15 @@ class TiledWeights:
         return out
 
 
+def _can_fuse(codec: str, descs) -> bool:
+    """Whether the decode-fused linear layer takes these blobs: every codebook
+    blob, and DFloat11 blobs of BF16 elements in blocks of 32 chunks or with a
+    single exponent (see lwc_linear_dfloat11)."""
+    return codec == "codebook" or all(
+        d.elem == lwc.LWC_ELEM_BF16 and (d.threads_per_block == 32 or d.flags & lwc.LWC_FLAG_SINGLE_EXPONENT)
+        for d in descs)
+
+
 def _gated_fused_rows(codec: str, cols: int) -> int:
     """Rows up to which ``ResidentModel.gated`` multiplies in the decode-fused
     linear layers rather than decoding both matrices for the dense kernel. us
@@ -729,7 +738,8 @@ class ResidentModel:
 
     def _matrices(self, layer: int, indices: tuple):
         """Launch arguments of some matrices of ``layer`` (kept: its blobs stay
-        where they are), their types: (Batch, LinearBatch, shapes, dtypes)."""
+        where they are), their types, and whether the decode-fused linear layer
+        takes them: (Batch, LinearBatch, shapes, dtypes, fusable)."""
         import torch
         key = (layer, indices)
         if key not in self._marshalled:
@@ -744,13 +754,14 @@ class ResidentModel:
             none = [None] * len(indices)
             self._marshalled[key] = (
                 lwc.Batch(descs, blobs, none), lwc.LinearBatch(descs, blobs, [s[1] for s in shapes], none, none, 0),
-                shapes, [torch.float16 if e == lwc.LWC_ELEM_FP16 else torch.bfloat16 for e in elems])
+                shapes, [torch.float16 if e == lwc.LWC_ELEM_FP16 else torch.bfloat16 for e in elems],
+                _can_fuse(self.codec, descs))
         return self._marshalled[key]
 
     def _decoded(self, layer: int, indices: tuple, stream, status=None):
         """The matrices ``indices`` of ``layer``, decoded into new buffers."""
         import torch
-        batch, _, shapes, dtypes = self._matrices(layer, indices)
+        batch, _, shapes, dtypes, _ = self._matrices(layer, indices)
         views = [torch.empty(s, dtype=t, device=self.device) for s, t in zip(shapes, dtypes)]
         fn = lwc.lwc_decode_dfloat11_batched if self.codec == "dfloat11" else lwc.lwc_decode_codebook_batched
         fn(batch.into(views), d_status=status, stream=stream)
@@ -758,10 +769,11 @@ class ResidentModel:
 
     def _gated(self, layer, gate, up, x, act, out, stream, status, route):
         import torch
-        _, linear, ((rows, cols), _), _ = self._matrices(layer, (gate, up))
+        _, linear, ((rows, cols), _), _, fusable = self._matrices(layer, (gate, up))
         M = x.numel() // cols
         if route == "auto":
-            route = "fused" if x.dtype == torch.bfloat16 and 1 <= M <= _gated_fused_rows(self.codec, cols) else "decode"
+            few = x.dtype == torch.bfloat16 and 1 <= M <= _gated_fused_rows(self.codec, cols)
+            route = "fused" if few and fusable else "decode"
         with _On(x.device, stream, (x, out, status)) as s:
             if route == "decode":
                 w_gate, w_up = self._decoded(layer, (gate, up), s, status)
@@ -789,7 +801,8 @@ class ResidentModel:
         route "fused": both products by the decode-fused linear layer (1 to 8
         rows, BF16), then the activation and the product; "decode": both
         matrices decoded into a temporary buffer, then ``gated_ffn``'s kernel;
-        "auto": the faster of the two by codec, rows and columns. Differentiable
+        "auto": the faster of the two by codec, rows and columns (the decode
+        route for blobs that the fused layer does not take). Differentiable
         for x: the backward pass decodes the matrices again instead of keeping
         them."""
         import torch

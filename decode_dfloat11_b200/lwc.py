@@ -33,6 +33,7 @@ LWC_DEVICE_BAD_CODE = 2
 LWC_DEVICE_BAD_OFFSET = 4
 LWC_DEVICE_TIMEOUT = 8
 LWC_DEVICE_BAD_TARGET = 16
+LWC_FLAG_SINGLE_EXPONENT = 1   # lwc_desc.flags
 LWC_ACT_SILU = 0
 LWC_ACT_GELU = 1
 LWC_ACT_GELU_TANH = 2

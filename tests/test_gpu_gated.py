@@ -549,3 +549,20 @@ def test_operands_of_compressed_forms_freed_before_the_stream_reads_them(codec, 
     x.requires_grad_(grad)
     got, _ = late(s, lambda x, t: model.cross_entropy(0, 0, x, t, reduction="none", stream=s), x, t)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [1, 2])
+def test_resident_model_of_other_blocks(M):
+    """DFloat11 blobs that the decode-fused linear layer does not take (blocks of 64 chunks)."""
+    N, K = 264, 320
+    wg, wu = (synth.normal_bf16((N, K), seed=s, sigma=0.05, outlier_frac=1e-3, device="cuda") for s in (1, 2))
+    model = layers.ResidentModel("dfloat11", "cuda")
+    model.add_layer_from_device("ffn", [wg, wu], threads_per_block=64)
+    x = torch.randn(M, K, generator=torch.Generator("cuda").manual_seed(M), device="cuda").bfloat16()
+    assert torch.equal(model.gated(0, 0, 1, x), layers.gated_ffn(x, wg, wu))
+    xg = x.clone().requires_grad_()
+    h = model.gated(0, 0, 1, xg)
+    h.backward(torch.ones_like(h))
+    assert torch.equal(xg.grad, layers.gated_ffn_backward(torch.ones_like(h), x, wg, wu, need=(True, False, False))[0])
+    with pytest.raises(lwc.LwcError, match="blocks of 32 chunks"):
+        model.gated(0, 0, 1, x, route="fused")

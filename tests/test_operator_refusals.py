@@ -3,6 +3,7 @@ before any device work (no GPU needed), and what their Python forms check."""
 import contextlib
 import ctypes
 
+import numpy as np
 import pytest
 
 from decode_dfloat11_b200 import build as lwc_build
@@ -163,3 +164,25 @@ def test_a_product_without_a_gradient_refuses_to_drop_one(monkeypatch):
     with torch.no_grad():
         assert tw.gated(0, 1, x).shape == (2, 128)
     assert tw.gated(0, 1, x.detach()).shape == (2, 128)
+
+
+@pytest.mark.parametrize("codec,params,values,route", [
+    ("dfloat11", {}, "spread", "fused"), ("dfloat11", dict(threads_per_block=64), "spread", "decode"),
+    ("dfloat11", dict(threads_per_block=64), "one exponent", "fused"), ("codebook", {}, "spread", "fused")])
+def test_one_row_of_any_blob_finds_a_route(monkeypatch, codec, params, values, route):
+    """The decode-fused linear layer takes DFloat11 blocks of 32 chunks only; "auto" decodes the others."""
+    torch = pytest.importorskip("torch")
+    w = np.random.default_rng(1).integers(0x3F00, 0x3F80 if values == "one exponent" else 0x4100, 64 * 64).astype(np.uint16)
+    model = layers.ResidentModel(codec, "cpu")
+    model.add_layer("ffn", layers.encode_many([w, w], codec, **params), [(64, 64)] * 2)
+    taken = []
+    for name in ("lwc_linear_dfloat11_batched", "lwc_linear_codebook_batched"):
+        monkeypatch.setattr(lwc, name, lambda *args, **kwargs: taken.append("fused"))
+    for name in ("lwc_decode_dfloat11_batched", "lwc_decode_codebook_batched"):
+        monkeypatch.setattr(lwc, name, lambda *args, **kwargs: taken.append("decode"))
+    for name in ("lwc_gated_product", "lwc_gated_forward"):
+        monkeypatch.setattr(lwc, name, lambda *args, **kwargs: None)
+    monkeypatch.setattr(layers, "_On", lambda *args: contextlib.nullcontext())
+    monkeypatch.setattr(layers, "_check_matrices", lambda x, **matrices: None)
+    model.gated(0, 0, 1, torch.zeros(1, 64, dtype=torch.bfloat16))
+    assert taken == [route]
