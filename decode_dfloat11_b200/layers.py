@@ -663,7 +663,6 @@ class ResidentModel:
         self.layers: list[dict] = []
         self.buffers = []
         self._batches: list[list] = []
-        self._marshalled: dict = {}   # (layer, indices): launch arguments of those matrices
 
     def add_layer(self, name: str, encoded, shapes) -> None:
         """encoded: [(desc, host blob)] of the layer's matrices, shapes their shapes."""
@@ -737,26 +736,29 @@ class ResidentModel:
                             status=status, route=route)
 
     def _matrices(self, layer: int, indices: tuple):
-        """Launch arguments of some matrices of ``layer`` (kept: its blobs stay
-        where they are), their types, and whether the decode-fused linear layer
-        takes them: (Batch, LinearBatch, shapes, dtypes, fusable)."""
+        """Launch arguments of some matrices of ``layer``, their types, and
+        whether the decode-fused linear layer takes them: (Batch, LinearBatch,
+        shapes, dtypes, fusable). Kept with the layer, and made again once its
+        blobs, descriptors or shapes are other ones (the arguments hold bare
+        addresses)."""
         import torch
-        key = (layer, indices)
-        if key not in self._marshalled:
-            data = self.layers[layer]
+        data = self.layers[layer]
+        descs, blobs = [data["descs"][i] for i in indices], [data["blobs"][i] for i in indices]
+        of = (*descs, *blobs, *[data["shapes"][i] for i in indices])
+        kept = data.setdefault("marshalled", {})
+        if indices not in kept or any(a is not b for a, b in zip(kept[indices][0], of)):
             shapes = [tuple(int(v) for v in data["shapes"][i]) for i in indices]
             if any(len(s) != 2 for s in shapes):
                 raise ValueError("the weight must be a rows x cols matrix")
-            elems = [data["descs"][i].elem if self.codec == "dfloat11" else lwc.LWC_ELEM_BF16 for i in indices]
+            elems = [d.elem if self.codec == "dfloat11" else lwc.LWC_ELEM_BF16 for d in descs]
             if lwc.LWC_ELEM_FP32 in elems:
                 raise ValueError("the matrix holds FP32 elements (BF16 and FP16 are taken)")
-            descs, blobs = [data["descs"][i] for i in indices], [data["blobs"][i] for i in indices]
             none = [None] * len(indices)
-            self._marshalled[key] = (
+            kept[indices] = of, (
                 lwc.Batch(descs, blobs, none), lwc.LinearBatch(descs, blobs, [s[1] for s in shapes], none, none, 0),
                 shapes, [torch.float16 if e == lwc.LWC_ELEM_FP16 else torch.bfloat16 for e in elems],
                 _can_fuse(self.codec, descs))
-        return self._marshalled[key]
+        return kept[indices][1]
 
     def _decoded(self, layer: int, indices: tuple, stream, status=None):
         """The matrices ``indices`` of ``layer``, decoded into new buffers."""

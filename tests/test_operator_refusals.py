@@ -186,3 +186,31 @@ def test_one_row_of_any_blob_finds_a_route(monkeypatch, codec, params, values, r
     monkeypatch.setattr(layers, "_check_matrices", lambda x, **matrices: None)
     model.gated(0, 0, 1, torch.zeros(1, 64, dtype=torch.bfloat16))
     assert taken == [route]
+
+
+def test_replaced_layers_are_marshalled_again():
+    """Launch arguments are bare addresses: those of a blob, or a layer, that was replaced must not be used."""
+    torch = pytest.importorskip("torch")
+
+    def layer(seed):
+        g = np.random.default_rng(seed)
+        return layers.encode_many([g.integers(0, 1 << 16, 64 * 8).astype(np.uint16) for _ in range(2)], "codebook")
+
+    model = layers.ResidentModel("codebook", "cpu")
+    model.add_layer("ffn", layer(1), [(64, 8)] * 2)
+    first = model._matrices(0, (0, 1))
+    assert model._matrices(0, (0, 1)) is first and model._matrices(0, (1,)) is not first
+    assert list(first[0].ins) == [b.data_ptr() for b in model.layers[0]["blobs"]]
+    # one blob
+    desc, blob = layer(2)[1]
+    model.layers[0]["descs"][1], model.layers[0]["blobs"][1] = desc, torch.from_numpy(blob)
+    assert list(model._matrices(0, (0, 1))[0].ins) == [b.data_ptr() for b in model.layers[0]["blobs"]]
+    # the whole layer, in another shape
+    model.layers.clear()
+    model.add_layer("ffn", layer(3), [(32, 16)] * 2)
+    again = model._matrices(0, (0, 1))
+    assert list(again[0].ins) == [b.data_ptr() for b in model.layers[0]["blobs"]] and again[2] == [(32, 16)] * 2
+    assert list(again[1].blobs) == list(again[0].ins)
+    # the same shape put in as another list
+    model.layers[0]["shapes"] = [(16, 32), (16, 32)]
+    assert model._matrices(0, (0, 1))[2] == [(16, 32)] * 2
