@@ -5,12 +5,19 @@
 //   P_iv = c_i (exp(z_iv - lse_i) - [v = t(i)]),  dx = P W,  dW = P^T x
 //
 // (x: M x K, W: V x K; c_i: the gradient of l_i.) Forward: a product kernel
-// whose epilogue keeps, per token and vocabulary tile, the largest logit, the
-// sum of exponentials under it, and the target's logit; a second kernel joins
-// the tiles. Backward: the vocabulary goes piece by piece; a piece's logits
-// are computed again, turned into P (16 bits) by the epilogue, and used at
-// once by two products, dW's rows of the piece and dx (summed over the pieces
-// in 32 bits).
+// whose epilogue keeps, per token and vocabulary tile, the largest logit and
+// the sum of exponentials under it, both of the words that are not the target,
+// and the target's logit; a second kernel joins the tiles. Backward: the
+// vocabulary goes piece by piece; a piece's logits are computed again, by the
+// same sums, turned into P (16 bits) by the epilogue, and used at once by two
+// products, dW's rows of the piece and dx (summed over the pieces in 32 bits).
+//
+// A token that is sure of its target has a loss and a p - 1 far below the
+// rounding of lse or of p, so neither is a difference of those: with R the
+// other words' sum of exp(z_v - z_t), the loss is log(1 + R) by log1p, and the
+// target's entry of P is c expm1(-loss). (Off by some 10^-4 in p - 1 at
+// K = 4096 as exp(z_t - lse) - 1 of two unlike sums, by the product's own
+// relative error this way.)
 //
 // A token whose target is ignore_index bears no loss and passes no gradient,
 // whatever its hidden state holds: its rows of P and of the x that dW reads
@@ -57,23 +64,19 @@ __device__ __forceinline__ int64_t target_of(int64_t t, int64_t ignore, uint64_t
 // where the products bound it (2048 tokens x 128256 words: 2.07 ms, not 1.85),
 // and nothing for few rows, where W's way from memory does.
 constexpr uint32_t kChunkSteps = 8, kChunkStepsFewRows = 4;
+uint32_t chunk_steps(uint64_t tokens) { return tokens > tc::kRows ? kChunkSteps : kChunkStepsFewRows; }
 
-struct XentStats {
-    struct Args {
-        float2 *part;   // rows x 2 n_tiles: (largest logit, sum of exp under it)
-        float *zt;      // the target's logit
-        const int64_t *targets;
-        int64_t ignore;
-        uint32_t rows, cols, n_tiles;
-    };
+// A thread's logits of a tile: its row, the columns 32 i + 16 side + j.
+struct Logits {
     float z[8][16];
-    __device__ __forceinline__ XentStats(const Args &, const tc::Tile &) {
+    __device__ __forceinline__ Logits() {
 #pragma unroll
         for (int i = 0; i < 8; i++)
 #pragma unroll
             for (int j = 0; j < 16; j++) z[i][j] = 0.0f;
     }
-    __device__ __forceinline__ void take(const Args &, const tc::Tile &t, bool) {
+    // adds an accumulator
+    __device__ __forceinline__ void add(const tc::Tile &t) {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const uint32_t c = 32 * i + 16 * t.side;
@@ -85,11 +88,24 @@ struct XentStats {
             }
         }
     }
+};
+
+struct XentStats : Logits {
+    struct Args {
+        float2 *part;   // rows x 2 n_tiles: (largest logit, sum of exp under it), without the target
+        float *zt;      // the target's logit
+        const int64_t *targets;
+        int64_t ignore;
+        uint32_t rows, cols, n_tiles;
+    };
+    __device__ __forceinline__ XentStats(const Args &, const tc::Tile &) {}
+    __device__ __forceinline__ void take(const Args &, const tc::Tile &t, bool) { add(t); }
     __device__ __forceinline__ void finish(const Args &E, const tc::Tile &t) {
         if (t.row >= E.rows) return;
         const uint32_t n0 = t.n * t.n_tile, width = min(t.n_tile, E.cols - n0);
         const int64_t tgt = target_of(E.targets[t.row], E.ignore, E.cols);
         const uint32_t at = tgt >= (int64_t)n0 && tgt < (int64_t)(n0 + width) ? (uint32_t)(tgt - n0) : 0xFFFFFFFFu;
+        float z_t = 0.0f;
         // four maxima and sums, so that no addition waits for the one before it
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {};
 #pragma unroll
@@ -97,10 +113,11 @@ struct XentStats {
 #pragma unroll
             for (int j = 0; j < 16; j++) {
                 const uint32_t c = 32 * i + 16 * t.side + j;
-                if (c >= width) z[i][j] = -INFINITY;
-                if (c == at) E.zt[t.row] = z[i][j];
+                if (c == at) z_t = z[i][j];
+                if (c >= width || c == at) z[i][j] = -INFINITY;
                 top[j & 3] = fmaxf(top[j & 3], z[i][j]);
             }
+        if (at != 0xFFFFFFFFu && ((at >> 4) & 1u) == t.side) E.zt[t.row] = z_t;
         const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         // nothing but -infinity: any finite base gives a sum of 0
         const float base = m == -INFINITY ? 0.0f : m;
@@ -113,29 +130,29 @@ struct XentStats {
     }
 };
 
-struct XentGrad {
+struct XentGrad : Logits {
     struct Args {
-        const float *lse, *coef;
+        const float *lse, *loss, *coef;
         const int64_t *targets;
         uint16_t *p;    // rows x cols, in panels
         int64_t first;  // the piece's first column of the vocabulary
         uint32_t rows, cols, padded, fp16;   // padded: cols filled up to whole panels, with zeros
     };
     __device__ __forceinline__ XentGrad(const Args &, const tc::Tile &) {}
-    __device__ __forceinline__ void finish(const Args &, const tc::Tile &) {}
-    __device__ __forceinline__ void take(const Args &E, const tc::Tile &t, bool) {
+    __device__ __forceinline__ void take(const Args &, const tc::Tile &t, bool) { add(t); }
+    __device__ __forceinline__ void finish(const Args &E, const tc::Tile &t) {
+        if (t.row >= E.rows) return;
         const uint32_t n0 = t.n * t.n_tile, end = min(E.padded, n0 + t.n_tile);
-        const bool live = t.row < E.rows;
-        const float c_i = live ? E.coef[t.row] : 0.0f, lse = live ? E.lse[t.row] : 0.0f;
-        const int64_t at = live ? E.targets[t.row] - E.first : -1;
-        for (uint32_t c = n0 + 16 * t.side; c < end; c += 32) {
-            uint32_t raw[16];
-            umma::tmem_ld16(t.taddr + (c - n0), raw);
-            if (!live) continue;
+        const float c_i = E.coef[t.row], lse = E.lse[t.row], hot = expm1f(-E.loss[t.row]);
+        const int64_t at = E.targets[t.row] - E.first;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t c = n0 + 32 * i + 16 * t.side;
+            if (c >= end) break;
             float v[16];
 #pragma unroll
             for (int j = 0; j < 16; j++) {
-                const float p = pow2((__uint_as_float(raw[j]) - lse) * kLog2e) - (at == (int64_t)(c + j) ? 1.0f : 0.0f);
+                const float p = at == (int64_t)(c + j) ? hot : pow2((z[i][j] - lse) * kLog2e);
                 v[j] = c_i == 0.0f || c + j >= E.cols ? 0.0f : p * c_i;
             }
             tc::store_panel(E.p, E.rows, t.row, c, end, E.fp16, v);
@@ -170,8 +187,14 @@ __global__ void __launch_bounds__(few::kWarps * 32)
                 z[0] = acc[0][r];
                 z[1] = v2 != v ? acc[1][r] : -INFINITY;
             }
-        if (lane < rows && target == (int64_t)v) zt[lane] = z[0];
-        if (lane < rows && v2 != v && target == (int64_t)v2) zt[lane] = z[1];
+        if (lane < rows && target == (int64_t)v) {
+            zt[lane] = z[0];
+            z[0] = -INFINITY;
+        }
+        if (lane < rows && v2 != v && target == (int64_t)v2) {
+            zt[lane] = z[1];
+            z[1] = -INFINITY;
+        }
         const float top = fmaxf(m, fmaxf(z[0], z[1])), base = top == -INFINITY ? 0.0f : top;
         s = s * pow2((m - base) * kLog2e) + pow2((z[0] - base) * kLog2e) + pow2((z[1] - base) * kLog2e);
         m = top;
@@ -213,10 +236,14 @@ __global__ void xent_join_kernel(const float2 *__restrict__ part, uint32_t parts
         }
         if (lane == 0) {
             const int64_t t = target_of(targets[row], ignore, vocab);
-            const float l = (m == -INFINITY ? 0.0f : m) + logf(s);
+            const float z_t = t >= 0 ? zt[row] : -INFINITY;
+            const float top = fmaxf(m, z_t), base = top == -INFINITY ? 0.0f : top;
+            const float l = base + logf(s * expf(m - base) + (t >= 0 ? expf(z_t - base) : 0.0f));
             lse[row] = l;
-            // (m - z_t) first: both are logits of one product, so their common part cancels exactly
-            loss[row] = t == -1 ? 0.0f : t == -2 ? NAN : (m == -INFINITY ? 0.0f : m) - zt[row] + logf(s);
+            // from differences of logits: both are of one product, so their common part cancels exactly
+            const float d = m - z_t;
+            const float v = d <= 0.0f ? log1pf(s * expf(d)) : d + logf(s + expf(-d));
+            loss[row] = t == -1 ? 0.0f : t == -2 || !isfinite(l) ? NAN : v;
             if (t == -2 && status) atomicOr(status, (uint32_t)LWC_DEVICE_BAD_TARGET);
         }
     }
@@ -359,7 +386,7 @@ lwc_status plan_forward(const lwc_xent *x, uint32_t *d_status, ForwardPlan &f) {
     p.n = x->vocab;
     p.k = x->hidden;
     p.fp16 = x->elem == LWC_ELEM_FP16;
-    p.chunk = x->tokens > tc::kRows ? kChunkSteps : kChunkStepsFewRows;
+    p.chunk = chunk_steps(x->tokens);
     p.status = d_status;
     const lwc_status st = tc::plan_product(p, false);
     if (st) return st;
@@ -368,12 +395,15 @@ lwc_status plan_forward(const lwc_xent *x, uint32_t *d_status, ForwardPlan &f) {
     return LWC_OK;
 }
 
-// Backward workspace: coef, alpha, x transposed (zeros where a token bears no
-// loss), a piece of P (both in panels), dx in FP32, parts of split products.
+// Backward workspace: coef, the losses and lse of a forward pass (where the
+// caller has no losses), alpha, x transposed (zeros where a token bears no
+// loss), a piece of P (both in panels; before it, in its place, the forward
+// pass's workspace), dx in FP32, parts of split products.
 struct BackwardPlan {
     uint64_t piece;
     uint32_t dx_width = 0;   // the tiles of dx: the same for every piece, since they share its sum
-    uint64_t alpha_off, xt_off, p_off, acc_off, part_off, total;
+    uint64_t loss_off, lse_off, alpha_off, xt_off, p_off, acc_off, part_off, total;
+    ForwardPlan forward;
 };
 
 // One piece: columns first .. first + width - 1 of the vocabulary.
@@ -391,6 +421,7 @@ lwc_status plan_piece(const lwc_xent *x, const BackwardPlan &b, const uint8_t *w
         z->n = round_up(width, 64);   // whole panels
         z->k = x->hidden;
         z->fp16 = fp16;
+        z->chunk = chunk_steps(x->tokens);   // the forward pass's sums: what they are off by cancels in z - lse
         z->status = d_status;
         st = tc::plan_product(*z, false);
     }
@@ -423,22 +454,29 @@ lwc_status plan_piece(const lwc_xent *x, const BackwardPlan &b, const uint8_t *w
     return st;
 }
 
-lwc_status plan_backward(const lwc_xent *x, bool want_dx, bool want_dw, BackwardPlan &b) {
+lwc_status plan_backward(const lwc_xent *x, bool want_dx, bool want_dw, bool have_loss, BackwardPlan &b) {
     const uint64_t M = x->tokens, V = x->vocab, K = x->hidden;
     // pieces of equal width, a multiple of the widest tile
     const uint64_t pieces = std::max<uint64_t>(1, (2 * M * V + kPieceBytes - 1) / kPieceBytes);
     b.piece = std::min(V, round_up((V + pieces - 1) / pieces, tc::kMaxCols));
-    b.alpha_off = round_up(M * 4, 256);
+    lwc_status st = LWC_OK;
+    b.forward.total = 0;
+    b.loss_off = b.alpha_off = round_up(M * 4, 256);
+    if (!have_loss) {
+        st = plan_forward(x, nullptr, b.forward);
+        if (st) return st;
+        b.lse_off = 2 * b.loss_off;
+        b.alpha_off = 3 * b.loss_off;
+    }
     b.xt_off = b.alpha_off + 256;
     b.p_off = b.xt_off + (want_dw ? round_up(tc::panel_bytes(K, M), 256) : 0);
-    b.acc_off = b.p_off + round_up(tc::panel_bytes(M, b.piece), 256);
+    b.acc_off = b.p_off + std::max(round_up(tc::panel_bytes(M, b.piece), 256), b.forward.total);
     uint64_t part = 0, acc = 0;
     // the widths that occur: a full piece and the last one
     for (const uint64_t width : {b.piece, V % b.piece}) {
         if (width == 0) break;
         Product dw, dx;
-        const lwc_status st =
-            plan_piece(x, b, nullptr, 0, width, nullptr, nullptr, want_dw ? &dw : nullptr, want_dx ? &dx : nullptr);
+        st = plan_piece(x, b, nullptr, 0, width, nullptr, nullptr, want_dw ? &dw : nullptr, want_dx ? &dx : nullptr);
         if (st) return st;
         if (want_dw) part = std::max(part, dw.part_bytes);
         if (want_dx) part = std::max(part, dx.part_bytes);
@@ -457,46 +495,13 @@ lwc_status launched(const char *what, cudaError_t err) {
     return LWC_OK;
 }
 
-}  // namespace
-}  // namespace lwc
-
-using namespace lwc;
-
-extern "C" {
-
-uint64_t lwc_xent_forward_workspace_bytes(const lwc_xent *x) {
-    ForwardPlan f;
-    if (check(x) || x->tokens == 0 || plan_forward(x, nullptr, f)) return 0;
-    clear_error();
-    return f.total;
-}
-
-lwc_status lwc_xent_forward(const lwc_xent *x, float *d_loss, float *d_lse, float *d_sum, float *d_mean, void *d_work,
-                            uint64_t work_bytes, uint32_t *d_status, lwc_stream_t stream) {
-    lwc_status st = check(x);
-    if (st) return st;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (x->tokens == 0) {
-        for (float *p : {d_sum, d_mean}) {
-            const cudaError_t err = p ? cudaMemsetAsync(p, 0, sizeof(float), s) : cudaSuccess;
-            if (err != cudaSuccess) return fail(LWC_ERR_CUDA, "output fill: %s", cudaGetErrorString(err));
-        }
-        clear_error();
-        return LWC_OK;
-    }
-    if (!d_loss || !d_lse) return fail(LWC_ERR_INVALID_ARG, "NULL device pointer");
-    st = check_words({d_loss, d_lse, d_sum, d_mean}, d_status, d_work);
-    if (st) return st;
-    ForwardPlan f;
-    st = plan_forward(x, d_status, f);
-    if (st) return st;
-    if (work_bytes < f.total)
-        return fail(LWC_ERR_INVALID_ARG, "workspace of %llu bytes, %llu needed", (unsigned long long)work_bytes,
-                    (unsigned long long)f.total);
-    uint8_t *work = static_cast<uint8_t *>(d_work);
+// The forward pass's launches; d_bad: where targets that are no words are reported, or NULL.
+lwc_status run_forward(const lwc_xent *x, const ForwardPlan &f, float *d_loss, float *d_lse, float *d_sum,
+                       float *d_mean, uint8_t *work, uint32_t *d_bad, cudaStream_t s) {
     float2 *part = reinterpret_cast<float2 *>(work);
     float *zt = reinterpret_cast<float *>(work + f.zt_off);
     uint32_t parts = f.few_blocks;
+    lwc_status st = LWC_OK;
     if (f.few_blocks) {
         const dim3 grid(f.few_blocks);
         const uint32_t threads = few::kWarps * 32;
@@ -520,28 +525,19 @@ lwc_status lwc_xent_forward(const lwc_xent *x, float *d_loss, float *d_lse, floa
     const uint64_t blocks = std::min<uint64_t>((x->tokens + 7) / 8, 148 * 8);
     st = launched("loss join",
                   tc::launch_next(xent_join_kernel, dim3((unsigned)blocks), 256, 0, 1, s, part, parts, zt,
-                                  x->targets, x->ignore_index, x->tokens, x->vocab, d_loss, d_lse, d_status));
+                                  x->targets, x->ignore_index, x->tokens, x->vocab, d_loss, d_lse, d_bad));
     if (!st && (d_sum || d_mean))
         st = launched("loss total", tc::launch_next(xent_total_kernel, dim3(1), 1024, 0, 1, s, d_loss, x->targets,
                                                     x->ignore_index, x->tokens, d_sum, d_mean));
-    if (st) return st;
-    clear_error();
-    return LWC_OK;
+    return st;
 }
 
-uint64_t lwc_xent_backward_workspace_bytes(const lwc_xent *x, int want_dx, int want_dhead) {
-    BackwardPlan b;
-    if (check(x) || x->tokens == 0 || plan_backward(x, want_dx != 0, want_dhead != 0, b)) return 0;
-    clear_error();
-    return b.total;
-}
-
-lwc_status lwc_xent_backward(const lwc_xent *x, const float *d_lse, const float *d_grad, uint64_t grad_stride,
-                             int mean, void *d_dx, void *d_dhead, void *d_work, uint64_t work_bytes,
-                             uint32_t *d_status, lwc_stream_t stream) {
+// d_loss: the forward pass's losses, or NULL (computed again).
+lwc_status backward(const lwc_xent *x, const float *d_lse, const float *d_loss, const float *d_grad,
+                    uint64_t grad_stride, int mean, void *d_dx, void *d_dhead, void *d_work, uint64_t work_bytes,
+                    uint32_t *d_status, cudaStream_t s) {
     lwc_status st = check(x);
     if (st) return st;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if ((reinterpret_cast<uintptr_t>(d_dx) | reinterpret_cast<uintptr_t>(d_dhead)) & 1u)
         return fail(LWC_ERR_MISALIGNED, "odd device pointer");
     if (x->tokens == 0) {
@@ -557,10 +553,10 @@ lwc_status lwc_xent_backward(const lwc_xent *x, const float *d_lse, const float 
         return LWC_OK;
     }
     if (!d_lse || !d_grad) return fail(LWC_ERR_INVALID_ARG, "NULL device pointer");
-    st = check_words({d_lse, d_grad}, d_status, d_work);
+    st = check_words({d_lse, d_loss, d_grad}, d_status, d_work);
     if (st) return st;
     BackwardPlan b;
-    st = plan_backward(x, d_dx != nullptr, d_dhead != nullptr, b);
+    st = plan_backward(x, d_dx != nullptr, d_dhead != nullptr, d_loss != nullptr, b);
     if (st) return st;
     if (work_bytes < b.total)
         return fail(LWC_ERR_INVALID_ARG, "workspace of %llu bytes, %llu needed", (unsigned long long)work_bytes,
@@ -571,6 +567,14 @@ lwc_status lwc_xent_backward(const lwc_xent *x, const float *d_lse, const float 
     float *acc = reinterpret_cast<float *>(work + b.acc_off), *part = reinterpret_cast<float *>(work + b.part_off);
     const uint32_t fp16 = x->elem == LWC_ELEM_FP16;
 
+    if (!d_loss) {
+        float *loss = reinterpret_cast<float *>(work + b.loss_off);
+        b.forward.z.status = d_status;
+        st = run_forward(x, b.forward, loss, reinterpret_cast<float *>(work + b.lse_off), nullptr, nullptr,
+                         work + b.p_off, nullptr, s);
+        if (st) return st;
+        d_loss = loss;
+    }
     st = launched("loss coefficients",
                   tc::launch_next(xent_coef_kernel, dim3(1), 1024, 0, 1, s, d_grad, grad_stride, x->targets,
                                   x->ignore_index, x->tokens, x->vocab, (uint32_t)(mean != 0), fp16, coef, alpha));
@@ -582,6 +586,7 @@ lwc_status lwc_xent_backward(const lwc_xent *x, const float *d_lse, const float 
         if (st) break;
         XentGrad::Args e;
         e.lse = d_lse;
+        e.loss = d_loss;
         e.coef = coef;
         e.targets = x->targets;
         e.p = reinterpret_cast<uint16_t *>(work + b.p_off);
@@ -621,6 +626,72 @@ lwc_status lwc_xent_backward(const lwc_xent *x, const float *d_lse, const float 
     if (st) return st;
     clear_error();
     return LWC_OK;
+}
+
+}  // namespace
+}  // namespace lwc
+
+using namespace lwc;
+
+extern "C" {
+
+uint64_t lwc_xent_forward_workspace_bytes(const lwc_xent *x) {
+    ForwardPlan f;
+    if (check(x) || x->tokens == 0 || plan_forward(x, nullptr, f)) return 0;
+    clear_error();
+    return f.total;
+}
+
+lwc_status lwc_xent_forward(const lwc_xent *x, float *d_loss, float *d_lse, float *d_sum, float *d_mean, void *d_work,
+                            uint64_t work_bytes, uint32_t *d_status, lwc_stream_t stream) {
+    lwc_status st = check(x);
+    if (st) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (x->tokens == 0) {
+        for (float *p : {d_sum, d_mean}) {
+            const cudaError_t err = p ? cudaMemsetAsync(p, 0, sizeof(float), s) : cudaSuccess;
+            if (err != cudaSuccess) return fail(LWC_ERR_CUDA, "output fill: %s", cudaGetErrorString(err));
+        }
+        clear_error();
+        return LWC_OK;
+    }
+    if (!d_loss || !d_lse) return fail(LWC_ERR_INVALID_ARG, "NULL device pointer");
+    st = check_words({d_loss, d_lse, d_sum, d_mean}, d_status, d_work);
+    if (st) return st;
+    ForwardPlan f;
+    st = plan_forward(x, d_status, f);
+    if (st) return st;
+    if (work_bytes < f.total)
+        return fail(LWC_ERR_INVALID_ARG, "workspace of %llu bytes, %llu needed", (unsigned long long)work_bytes,
+                    (unsigned long long)f.total);
+    st = run_forward(x, f, d_loss, d_lse, d_sum, d_mean, static_cast<uint8_t *>(d_work), d_status, s);
+    if (st) return st;
+    clear_error();
+    return LWC_OK;
+}
+
+uint64_t lwc_xent_backward_workspace_bytes(const lwc_xent *x, int want_dx, int want_dhead) {
+    BackwardPlan b;
+    if (check(x) || x->tokens == 0 || plan_backward(x, want_dx != 0, want_dhead != 0, false, b)) return 0;
+    clear_error();
+    return b.total;
+}
+
+lwc_status lwc_xent_backward(const lwc_xent *x, const float *d_lse, const float *d_grad, uint64_t grad_stride,
+                             int mean, void *d_dx, void *d_dhead, void *d_work, uint64_t work_bytes,
+                             uint32_t *d_status, lwc_stream_t stream) {
+    return backward(x, d_lse, nullptr, d_grad, grad_stride, mean, d_dx, d_dhead, d_work, work_bytes, d_status,
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+lwc_status lwc_xent_backward_losses(const lwc_xent *x, const float *d_lse, const float *d_loss, const float *d_grad,
+                                    uint64_t grad_stride, int mean, void *d_dx, void *d_dhead, void *d_work,
+                                    uint64_t work_bytes, uint32_t *d_status, lwc_stream_t stream) {
+    const lwc_status st = check(x);
+    if (st) return st;
+    if (x->tokens && (d_dx || d_dhead) && !d_loss) return fail(LWC_ERR_INVALID_ARG, "NULL device pointer");
+    return backward(x, d_lse, d_loss, d_grad, grad_stride, mean, d_dx, d_dhead, d_work, work_bytes, d_status,
+                    reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -329,7 +329,7 @@ def _flat_targets(targets):
 
 
 def _xent_forward(x, head, targets, ignore_index, reduction, stream, status):
-    """(the loss, reduced or per token, and the lse per token)."""
+    """(the loss, reduced or per token, the losses per token and the lse per token)."""
     import torch
     with _On(x.device, stream, (x, head, targets, status)) as s:
         p, keep = _xent_problem(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), head, _flat_targets(targets),
@@ -340,28 +340,33 @@ def _xent_forward(x, head, targets, ignore_index, reduction, stream, status):
         work = _workspace(lwc.lwc_xent_forward_workspace_bytes(p), x.device)
         lwc.lwc_xent_forward(p, loss, lse, total if reduction == "sum" else None, total if reduction == "mean" else None,
                              work, work.numel(), status, s)
-    return loss if reduction == "none" else total, lse
+    return loss if reduction == "none" else total, loss, lse
 
 
-def _xent_backward(grad, lse, x, w_head, targets, ignore_index, reduction, need, stream, status):
-    with _On(x.device, stream, (grad, lse, x, w_head, targets, status)) as s:
+def _xent_backward(grad, lse, loss, x, w_head, targets, ignore_index, reduction, need, stream, status):
+    with _On(x.device, stream, (grad, lse, loss, x, w_head, targets, status)) as s:
         p, keep = _xent_problem(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), w_head, _flat_targets(targets),
                                 ignore_index)
         grad, lse = grad.contiguous(), lse.contiguous()
         dx = x.new_empty(x.shape) if need[0] else None
         dw = w_head.new_empty(w_head.shape) if need[1] else None
         work = _workspace(lwc.lwc_xent_backward_workspace_bytes(p, *need), x.device)
-        lwc.lwc_xent_backward(p, lse, grad, 1 if reduction == "none" else 0, reduction == "mean", dx, dw, work,
-                              work.numel(), status, s)
+        rest = (grad, 1 if reduction == "none" else 0, reduction == "mean", dx, dw, work, work.numel(), status, s)
+        if loss is None:
+            lwc.lwc_xent_backward(p, lse, *rest)
+        else:
+            lwc.lwc_xent_backward_losses(p, lse, loss.contiguous(), *rest)
     return dx, dw
 
 
 def linear_cross_entropy_backward(grad, lse, x, w_head, targets, ignore_index: int = -100, reduction: str = "mean",
-                                  need=(True, True), stream=None, status=None):
+                                  need=(True, True), stream=None, status=None, loss=None):
     """(dx, dw_head) of ``linear_cross_entropy`` from the gradient of its
     result and the lse that it returned; ``need`` says which are computed
-    (None for the other). Makes plain calls on one stream, so it can be
-    captured into a CUDA graph."""
+    (None for the other). ``loss``: the losses per token (reduction "none"
+    returns them), if there are; the result is the same without them, but
+    they are computed again, which costs a forward pass. Makes plain calls on
+    one stream, so it can be captured into a CUDA graph."""
     import torch
     _check_xent(x, w_head, targets, reduction)
     rows = x.shape[:-1] if reduction == "none" else ()
@@ -369,7 +374,9 @@ def linear_cross_entropy_backward(grad, lse, x, w_head, targets, ignore_index: i
         raise ValueError(f"grad must be a {tuple(rows)} FP32 tensor on {x.device}")
     if tuple(lse.shape) != tuple(x.shape[:-1]) or lse.dtype != torch.float32 or lse.device != x.device:
         raise ValueError(f"lse must be a {tuple(x.shape[:-1])} FP32 tensor on {x.device}")
-    return _xent_backward(grad, lse, x, w_head, targets, ignore_index, reduction, need, stream, status)
+    if loss is not None and (loss.shape != lse.shape or loss.dtype != torch.float32 or loss.device != x.device):
+        raise ValueError(f"loss must be a {tuple(x.shape[:-1])} FP32 tensor on {x.device}")
+    return _xent_backward(grad, lse, loss, x, w_head, targets, ignore_index, reduction, need, stream, status)
 
 
 def _check_xent(x, w_head, targets, reduction):
@@ -411,7 +418,7 @@ def linear_cross_entropy(x, w_head, targets, ignore_index: int = -100, reduction
         with _On(x.device, stream, (x, w_head, targets, status)):
             loss, lse = _functions()["xent"].apply(x, w_head, targets, ignore_index, reduction, status)
     else:
-        loss, lse = _xent_forward(x, w_head, targets, ignore_index, reduction, stream, status)
+        loss, _, lse = _xent_forward(x, w_head, targets, ignore_index, reduction, stream, status)
     return (loss, lse) if return_lse else loss
 
 
@@ -446,17 +453,19 @@ def _functions():
     class Xent(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, w_head, targets, ignore_index, reduction, status):
-            loss, lse = _xent_forward(x, w_head, targets, ignore_index, reduction, None, status)
-            ctx.save_for_backward(x, w_head, targets, lse)
+            result, loss, lse = _xent_forward(x, w_head, targets, ignore_index, reduction, None, status)
+            if reduction == "none":
+                result = loss.clone()   # which the caller may change in place
+            ctx.save_for_backward(x, w_head, targets, lse, loss)
             ctx.ignore_index, ctx.reduction, ctx.status = ignore_index, reduction, status
             ctx.mark_non_differentiable(lse)
-            return loss, lse
+            return result, lse
 
         @staticmethod
         def backward(ctx, grad, _):
             once()
-            x, w_head, targets, lse = ctx.saved_tensors
-            dx, dw = _xent_backward(grad, lse, x, w_head, targets, ctx.ignore_index, ctx.reduction,
+            x, w_head, targets, lse, loss = ctx.saved_tensors
+            dx, dw = _xent_backward(grad, lse, loss, x, w_head, targets, ctx.ignore_index, ctx.reduction,
                                     ctx.needs_input_grad[:2], None, ctx.status)
             return dx, dw, None, None, None, None
 
@@ -483,19 +492,21 @@ def _functions():
             with _On(x.device) as s:
                 (w,) = model._decoded(layer, (index,), s, status)
                 _check_xent(x, w, targets, reduction)
-                loss, lse = _xent_forward(x, w, targets, ignore_index, reduction, None, status)
-            ctx.save_for_backward(x, targets, lse)
+                result, loss, lse = _xent_forward(x, w, targets, ignore_index, reduction, None, status)
+                if reduction == "none":
+                    result = loss.clone()
+            ctx.save_for_backward(x, targets, lse, loss)
             ctx.args = (model, layer, index, ignore_index, reduction, status)
-            return loss
+            return result
 
         @staticmethod
         def backward(ctx, grad):
             once()
             model, layer, index, ignore_index, reduction, status = ctx.args
-            x, targets, lse = ctx.saved_tensors
+            x, targets, lse, loss = ctx.saved_tensors
             with _On(x.device) as s:
                 (w,) = model._decoded(layer, (index,), s, status)
-                dx = _xent_backward(grad, lse, x, w, targets, ignore_index, reduction, (True, False), None, status)[0]
+                dx = _xent_backward(grad, lse, loss, x, w, targets, ignore_index, reduction, (True, False), None, status)[0]
             return dx, None, None, None, None, None, None, None
 
     _FUNCTIONS.update(gated=Gated, xent=Xent, resident_gated=ResidentGated, resident_xent=ResidentXent)

@@ -56,6 +56,7 @@ EXPORTED = (
     "lwc_gemm_codebook_batched",
     "lwc_gated_forward", "lwc_gated_backward_workspace_bytes", "lwc_gated_backward", "lwc_gated_product",
     "lwc_xent_forward_workspace_bytes", "lwc_xent_forward", "lwc_xent_backward_workspace_bytes", "lwc_xent_backward",
+    "lwc_xent_backward_losses",
     "lwc_selftest_bounded_wait", "lwc_status_string",
     "lwc_last_error", "lwc_version",
 )
@@ -170,8 +171,9 @@ def load():
     L.lwc_xent_forward.argtypes = [X, _P, _P, _P, _P, _P, _u64, _P, _P]
     L.lwc_xent_backward_workspace_bytes.argtypes = [X, ctypes.c_int, ctypes.c_int]
     L.lwc_xent_backward.argtypes = [X, _P, _P, _u64, ctypes.c_int, _P, _P, _P, _u64, _P, _P]
+    L.lwc_xent_backward_losses.argtypes = [X, _P, _P, _P, _u64, ctypes.c_int, _P, _P, _P, _u64, _P, _P]
     for name in ("lwc_gated_forward", "lwc_gated_backward", "lwc_gated_product", "lwc_xent_forward",
-                 "lwc_xent_backward"):
+                 "lwc_xent_backward", "lwc_xent_backward_losses"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("lwc_gated_backward_workspace_bytes", "lwc_xent_forward_workspace_bytes",
                  "lwc_xent_backward_workspace_bytes"):
@@ -455,6 +457,14 @@ def lwc_xent_backward(x: lwc_xent, d_lse, d_grad, grad_stride: int, mean: bool, 
     _check(load().lwc_xent_backward(ctypes.byref(x), _addr(d_lse), _addr(d_grad), grad_stride, int(bool(mean)),
                                     _addr(d_dx), _addr(d_dhead), _addr(d_work), work_bytes, _addr(d_status),
                                     _stream(stream)))
+
+
+def lwc_xent_backward_losses(x: lwc_xent, d_lse, d_loss, d_grad, grad_stride: int, mean: bool, d_dx, d_dhead, d_work,
+                             work_bytes: int, d_status=None, stream=None) -> None:
+    """lwc_xent_backward with lwc_xent_forward's losses, which it computes again otherwise."""
+    _check(load().lwc_xent_backward_losses(ctypes.byref(x), _addr(d_lse), _addr(d_loss), _addr(d_grad), grad_stride,
+                                           int(bool(mean)), _addr(d_dx), _addr(d_dhead), _addr(d_work), work_bytes,
+                                           _addr(d_status), _stream(stream)))
 
 
 def lwc_selftest_bounded_wait(d_status, polls: int, arrive: bool, stream=None) -> None:

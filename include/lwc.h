@@ -436,8 +436,10 @@ typedef struct lwc_xent {
 
 /* d_loss, d_lse: one FP32 value per token. d_sum, d_mean (each optional): one
  * FP32 value, the sum of the losses, and that over max(tokens whose target is
- * not ignore_index, 1) (so a batch of ignored tokens has mean 0). Logits and sums are FP32. Repeats bit for bit. Workspace as for
- * lwc_gated_backward. */
+ * not ignore_index, 1) (so a batch of ignored tokens has mean 0). Logits and
+ * sums are FP32; a loss is right relative to itself up to its logits' errors,
+ * however small (log(1 + R), R the other words' sum of exp(z_v - z_t)).
+ * Repeats bit for bit. Workspace as for lwc_gated_backward. */
 LWC_API uint64_t lwc_xent_forward_workspace_bytes(const lwc_xent *x);
 LWC_API lwc_status lwc_xent_forward(const lwc_xent *x, float *d_loss, float *d_lse, float *d_sum, float *d_mean,
                                     void *d_work, uint64_t work_bytes, uint32_t *d_status, lwc_stream_t stream);
@@ -455,6 +457,15 @@ LWC_API uint64_t lwc_xent_backward_workspace_bytes(const lwc_xent *x, int want_d
 LWC_API lwc_status lwc_xent_backward(const lwc_xent *x, const float *d_lse, const float *d_grad, uint64_t grad_stride,
                                      int mean, void *d_dx, void *d_dhead, void *d_work, uint64_t work_bytes,
                                      uint32_t *d_status, lwc_stream_t stream);
+
+/* The same, bit for bit, with d_loss, lwc_xent_forward's losses for the same
+ * x. The target's entry of P is c_i expm1(-loss_i), right relative to itself
+ * however sure a token is of its target, where exp(z - lse) - 1 would be
+ * lse's rounding; lwc_xent_backward has to compute the losses once more. */
+LWC_API lwc_status lwc_xent_backward_losses(const lwc_xent *x, const float *d_lse, const float *d_loss,
+                                            const float *d_grad, uint64_t grad_stride, int mean, void *d_dx,
+                                            void *d_dhead, void *d_work, uint64_t work_bytes, uint32_t *d_status,
+                                            lwc_stream_t stream);
 
 /* ---- device encoders ------------------------------------------------------ */
 

@@ -435,3 +435,113 @@ def test_a_block_and_the_loss_together():
     assert abs(float(loss.detach()) - float(want.detach())) <= 8 * 2.0 ** -8 * float(want.detach())
     for v, r in zip(leaves, ref):
         assert float((v.grad.double() - r.grad).norm()) <= 8 * 2.0 ** -8 * float(r.grad.norm())
+
+
+def confident(M, V, K, dtype, first=0.0):
+    """Tokens that are surer and surer of their target: 1 - p from 1e-2 down to below 1e-8 (z_t = `lean` and a
+    spread of one; the other words' sum of exponentials is about V e^(1/2))."""
+    g = torch.Generator("cuda").manual_seed(23)
+    w = torch.randn(V, K, generator=g, device="cuda").mul_(K ** -0.5).to(dtype)
+    t = torch.randint(0, V, (M,), generator=g, device="cuda")
+    lean = torch.linspace(first or 12.0, 28.0, M, device="cuda")[:, None]
+    x = (torch.randn(M, K, generator=g, device="cuda") + lean * w[t].float()).to(dtype)
+    return x, w, t
+
+
+def confident_bound(x, w, t, c):
+    """dx in 64 bits and its bound, relative to 1 - p. With q_i = 1 - p_i,t and P' the computed P:
+
+    z' - z <= e_z = (gamma_512 + 16 u) S: parts of at most 512 terms, added in FP32. Every word's P is off by at
+    most a factor exp(2 e), e = max_v e_z + 2^-22 (1 + |lse|) (the logits' errors, those of the target's logit, the
+    lse rounded to FP32); so is the target's own entry -q, which depends on differences of logits alone. Then the
+    roundings: P to 16 bits (half a step; FP16's subnormal numbers 2^-25 / 2^14 of the largest c), the FP32 sum
+    over V words, the result."""
+    half, tiny = HALF[x.dtype], TINY[x.dtype]
+    x, w = x.double(), w.double()
+    z = x @ w.T
+    e = ((gamma(512) + 16 * U) * (x.abs() @ w.abs().T)).amax(1) + 2.0 ** -22 * (1 + torch.logsumexp(z, 1).abs())
+    others = z.scatter(1, t[:, None], -float("inf"))
+    # log sum over the others less z_t: q / (1 - q) = exp(rest)
+    rest = torch.logsumexp(others, 1) - z.gather(1, t[:, None])[:, 0]
+    q = torch.sigmoid(rest)
+    p = torch.exp(others - z.gather(1, t[:, None])) * torch.sigmoid(-rest)[:, None]
+    P = c * p.scatter(1, t[:, None], -q[:, None])
+    off = torch.expm1(2 * e)[:, None] + half * torch.exp(2 * e)[:, None]
+    eP = P.abs() * off + (c * 2.0 ** -38 if half < 2.0 ** -8 else 0.0)
+    dx = P @ w
+    err = eP @ w.abs() + (gamma(w.shape[0]) + 2.0 ** -18) * ((P.abs() + eP) @ w.abs())
+    return q, dx, err + half * (dx.abs() + err) + tiny
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,K", [(300, 4096), (100, 4096), (40, 1000)])
+def test_gradients_of_confident_tokens(M, K, dtype):
+    """The target's entry, p - 1, is right relative to itself however close p is to 1."""
+    x, w, t = confident(M, 2000, K, dtype)
+    c = 65536.0   # as a loss is scaled for FP16
+    q, want, tol = confident_bound(x, w, t, c)
+    assert float(q.min()) < 1e-8 and float(q.max()) > 1e-3
+    leaf = x.clone().requires_grad_()
+    layers.linear_cross_entropy(leaf, w, t, reduction="sum").mul(c).backward()
+    # the bound says something: a few hundredths of a row's size, but for the tails of FP16's surest tokens
+    sure = q > (1e-6 if dtype == torch.float16 else 0)
+    assert bool((tol.norm(dim=1) < 0.05 * want.norm(dim=1))[sure].all())
+    close(leaf.grad, want, tol)
+
+
+@pytest.mark.parametrize("lean", [14.0, 19.5, 23.5, 27.0])
+def test_the_gradient_of_one_confident_token(lean):
+    """One row: its forward pass runs on the FP32 units, its backward pass on the tensor cores."""
+    x, w, t = confident(1, 2000, 4096, torch.bfloat16, first=lean)
+    q, want, tol = confident_bound(x, w, t, 1.0)
+    leaf = x.clone().requires_grad_()
+    layers.linear_cross_entropy(leaf, w, t).backward()
+    close(leaf.grad, want, tol)
+
+
+def test_losses_of_confident_tokens():
+    """The loss itself is right relative to itself, down to 1e-8."""
+    for M in (300, 100, 2, 1):
+        x, w, t = confident(M, 2000, 4096, torch.bfloat16, first=20.0)
+        q, _, _ = confident_bound(x, w, t, 1.0)
+        z = x.double() @ w.double().T
+        e = ((gamma(512) + 16 * U) * (x.double().abs() @ w.double().abs().T)).amax(1) + 2.0 ** -20
+        loss = layers.linear_cross_entropy(x, w, t, reduction="none")
+        want = -torch.log1p(-q)
+        close(loss, want, torch.expm1(2 * e) * want)
+
+
+def test_gradients_of_far_logits():
+    """Logits of thousands: every word's share is as right as the differences of the logits are."""
+    M, V, K = 300, 500, 4096
+    x, w, t = inputs(M, V, K, torch.bfloat16, seed=24, ignored=0.0)
+    x = (x.float() + 2000 * K ** -0.5).bfloat16()   # a direction that all words share
+    w = (w.float() + K ** -0.5).bfloat16()
+    q, want, tol = confident_bound(x, w, t, 1.0)
+    leaf = x.clone().requires_grad_()
+    layers.linear_cross_entropy(leaf, w, t, reduction="sum").backward()
+    close(leaf.grad, want, tol)
+
+
+@pytest.mark.parametrize("M", [1, 3, 100, 300])
+def test_the_losses_given_or_computed_again_are_the_same(M):
+    """The explicit backward pass without the losses per token computes them; autograd keeps them, whatever
+    becomes of the result."""
+    x, w, t = inputs(M, 900, 200, torch.bfloat16, seed=25)
+    losses, lse = layers.linear_cross_entropy(x, w, t, reduction="none", return_lse=True)
+    for reduction in ("none", "sum", "mean"):
+        up = torch.linspace(0.5, 2, M, device="cuda") if reduction == "none" else torch.tensor(1.5, device="cuda")
+        want = layers.linear_cross_entropy_backward(up, lse, x, w, t, reduction=reduction)
+        strided = torch.stack([losses, losses], 1)[:, 0]
+        for loss in (losses, strided):
+            got = layers.linear_cross_entropy_backward(up, lse, x, w, t, reduction=reduction, loss=loss)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        leaves = [x.clone().requires_grad_(), w.clone().requires_grad_()]
+        result = layers.linear_cross_entropy(*leaves, t, reduction=reduction)
+        result.mul_(2)   # in place
+        result.backward(up)
+        want = layers.linear_cross_entropy_backward(2 * up, lse, x, w, t, reduction=reduction)
+        assert all(torch.equal(a.grad, b) for a, b in zip(leaves, want))
+    for bad in (losses.double(), losses[:0], losses.cpu()):
+        with pytest.raises(ValueError, match="loss must be"):
+            layers.linear_cross_entropy_backward(up, lse, x, w, t, loss=bad)

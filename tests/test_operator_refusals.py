@@ -214,3 +214,17 @@ def test_replaced_layers_are_marshalled_again():
     # the same shape put in as another list
     model.layers[0]["shapes"] = [(16, 32), (16, 32)]
     assert model._matrices(0, (0, 1))[2] == [(16, 32)] * 2
+
+
+def test_xent_backward_from_losses():
+    back = lwc.lwc_xent_backward_losses
+    for status, change in XENT:
+        refused(status, back, xent(**change), P, P, P, 0, True, P, P, P, 1 << 30)
+    x = xent()
+    refused(lwc.LWC_ERR_INVALID_ARG, back, x, None, P, P, 0, True, P, P, P, 1 << 30)
+    refused(lwc.LWC_ERR_INVALID_ARG, back, x, P, None, P, 0, True, P, P, P, 1 << 30)
+    refused(lwc.LWC_ERR_INVALID_ARG, back, x, P, P, None, 0, True, P, P, P, 1 << 30)
+    refused(lwc.LWC_ERR_MISALIGNED, back, x, P, P + 2, P, 0, True, P, P, P, 1 << 30)
+    refused(lwc.LWC_ERR_MISALIGNED, back, x, P, P, P, 0, True, P + 1, P, P, 1 << 30)
+    refused(lwc.LWC_ERR_MISALIGNED, back, x, P, P, P, 0, True, P, P, P + 16, 1 << 30)
+    back(x, P, None, P, 0, True, None, None, None, 0)
