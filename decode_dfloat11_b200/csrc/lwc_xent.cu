@@ -285,6 +285,10 @@ __global__ void xent_total_kernel(const float *__restrict__ loss, const int64_t 
 // P has the scale of the probabilities whatever the loss is divided by, and
 // where every token counts alike, coef is 1, so that the largest entry of a
 // row, p - 1 at the target, is not rounded by a factor that all rows share.
+// The maximum is of the finite |c|: an infinite or NaN gradient spoils its own
+// token's row of dx (and dW), not the scale of the others.
+// FP16: a token whose |c| is below 2^-12 of the largest has probabilities below
+// 2^-16 among FP16's subnormal numbers (a step of 2^-38 of the largest |c|).
 // One block.
 __global__ void xent_coef_kernel(const float *__restrict__ grad, uint64_t grad_stride,
                                  const int64_t *__restrict__ targets, int64_t ignore, uint64_t rows, uint64_t vocab,
@@ -297,7 +301,8 @@ __global__ void xent_coef_kernel(const float *__restrict__ grad, uint64_t grad_s
     for (uint64_t i = threadIdx.x; i < rows; i += blockDim.x) {
         const int64_t t = target_of(targets[i], ignore, vocab);
         n += t != -1;
-        if (t >= 0) top = fmaxf(top, fabsf(grad[i * grad_stride]));
+        const float g = t >= 0 ? fabsf(grad[i * grad_stride]) : 0.0f;
+        if (isfinite(g)) top = fmaxf(top, g);
     }
     for (uint32_t d = 16; d; d >>= 1) {
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));

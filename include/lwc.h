@@ -450,9 +450,11 @@ LWC_API lwc_status lwc_xent_forward(const lwc_xent *x, float *d_loss, float *d_l
  *     dx = P head,  dhead = P^T x
  * into contiguous matrices of type `elem`; either may be NULL. The logits are
  * computed again, a piece of the vocabulary at a time; P is rounded to `elem`
- * once, scaled by a power of two so that FP16 keeps small probabilities; sums
- * are FP32. Repeats bit for bit. d_lse: lwc_xent_forward's, for the same x.
- * With tokens = 0, dhead is zeros. */
+ * once, divided by the largest finite |c_i| (and, for FP16, times 2^14, so that
+ * small probabilities keep their digits: entries below 2^-28 of that |c_i| are
+ * subnormal numbers, in steps of 2^-38); sums are FP32. An infinite or NaN c_i
+ * spoils dhead and its own row of dx only. Repeats bit for bit. d_lse:
+ * lwc_xent_forward's, for the same x. With tokens = 0, dhead is zeros. */
 LWC_API uint64_t lwc_xent_backward_workspace_bytes(const lwc_xent *x, int want_dx, int want_dhead);
 LWC_API lwc_status lwc_xent_backward(const lwc_xent *x, const float *d_lse, const float *d_grad, uint64_t grad_stride,
                                      int mean, void *d_dx, void *d_dhead, void *d_work, uint64_t work_bytes,

@@ -545,3 +545,26 @@ def test_the_losses_given_or_computed_again_are_the_same(M):
     for bad in (losses.double(), losses[:0], losses.cpu()):
         with pytest.raises(ValueError, match="loss must be"):
             layers.linear_cross_entropy_backward(up, lse, x, w, t, loss=bad)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_an_infinite_gradient_stays_in_its_row(bad, dtype):
+    x, w, t = inputs(300, 500, 64, dtype, seed=26)
+    g = torch.Generator("cuda").manual_seed(2)
+    grad = torch.randn(300, generator=g, device="cuda")
+    _, lse = layers.linear_cross_entropy(x, w, t, return_lse=True)
+    rows = (t != IGNORE).nonzero()[[0, 100], 0]
+    zero, spoilt = grad.clone(), grad.clone()
+    zero[rows], spoilt[rows] = 0.0, bad
+    spoilt[t == IGNORE] = bad   # never looked at
+    want, _ = layers.linear_cross_entropy_backward(zero, lse, x, w, t, reduction="none")
+    dx, dw = layers.linear_cross_entropy_backward(spoilt, lse, x, w, t, reduction="none")
+    keep = torch.ones(300, dtype=torch.bool, device="cuda")
+    keep[rows] = False
+    assert torch.equal(dx[keep], want[keep]) and not dx[t == IGNORE].any()
+    assert not bool(dx[rows].isfinite().any()) and not bool(dw.isfinite().all())
+    # one value for all tokens: nothing but ignored tokens is left
+    for reduction in ("sum", "mean"):
+        dx, _ = layers.linear_cross_entropy_backward(torch.tensor(bad, device="cuda"), lse, x, w, t, reduction=reduction)
+        assert not dx[t == IGNORE].any() and not bool(dx[t != IGNORE].isfinite().any())
