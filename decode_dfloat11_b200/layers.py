@@ -153,6 +153,14 @@ def _check_matrices(x, **matrices):
             raise ValueError(f"{name} must have x's type and device ({x.dtype}, {x.device})")
 
 
+def _refuse_tangents(*tensors):
+    """Forward-mode differentiation does not pass through the kernels: a dual
+    tensor's tangent would be dropped without a word."""
+    from torch.autograd import forward_ad
+    if forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("the operator has no forward-mode derivative (a dual tensor was given)")
+
+
 def _rows(t):
     """(t, row stride) of a matrix whose rows the kernels can read where they
     are (16-byte aligned, elements adjacent), else of a copy laid out so."""
@@ -230,6 +238,7 @@ def _gated_problem(x2, w_gate, w_up, act):
 
 def _check_gated(x, w_gate, w_up, act):
     _act_id(act)
+    _refuse_tangents(x, w_gate, w_up)
     _check_matrices(x, w_gate=w_gate)
     if w_up.shape != w_gate.shape:
         raise ValueError(f"w_gate and w_up differ in shape: {tuple(w_gate.shape)}, {tuple(w_up.shape)}")
@@ -267,6 +276,7 @@ def gated_ffn_backward(dh, x, w_gate, w_up, act: str = "silu", need=(True, True,
     result; ``need`` says which are computed (None for the others). Both
     projections are computed again from x. Makes plain calls on one stream, so
     it can be captured into a CUDA graph."""
+    _refuse_tangents(dh)
     _check_gated(x, w_gate, w_up, act)
     if tuple(dh.shape) != (*x.shape[:-1], w_gate.shape[0]) or dh.dtype != x.dtype or dh.device != x.device:
         raise ValueError(f"dh must be {(*x.shape[:-1], w_gate.shape[0])}, of x's type and device")
@@ -284,7 +294,7 @@ def gated_ffn(x, w_gate, w_up, act: str = "silu", out=None, stream=None, status=
     the caller orders it after what makes the inputs). ``status``: optional
     device status word.
 
-    Differentiable for x, w_gate and w_up (once); the two projections are not
+    Differentiable for x, w_gate and w_up (once, in reverse mode); the two projections are not
     kept but computed again in the backward pass, so the matrices must still
     hold the same values there. Matrices decoded into a reused buffer do not:
     use ``ResidentModel.gated``, which decodes them again. To capture a backward
@@ -368,6 +378,7 @@ def linear_cross_entropy_backward(grad, lse, x, w_head, targets, ignore_index: i
     they are computed again, which costs a forward pass. Makes plain calls on
     one stream, so it can be captured into a CUDA graph."""
     import torch
+    _refuse_tangents(grad)
     _check_xent(x, w_head, targets, reduction)
     rows = x.shape[:-1] if reduction == "none" else ()
     if tuple(grad.shape) != tuple(rows) or grad.dtype != torch.float32 or grad.device != x.device:
@@ -380,6 +391,7 @@ def linear_cross_entropy_backward(grad, lse, x, w_head, targets, ignore_index: i
 
 
 def _check_xent(x, w_head, targets, reduction):
+    _refuse_tangents(x, w_head)
     _check_matrices(x, w_head=w_head)
     _check_targets(x, targets, reduction)
 
@@ -407,7 +419,7 @@ def linear_cross_entropy(x, w_head, targets, ignore_index: int = -100, reduction
     tokens not ignored (0 if there is none); with ``return_lse`` also the log
     of each token's sum of exponentials (not differentiable).
 
-    Differentiable for x and w_head (once); the backward pass computes the
+    Differentiable for x and w_head (once, in reverse mode); the backward pass computes the
     logits again, a piece of the vocabulary at a time, so w_head must still
     hold the same values there (``ResidentModel.cross_entropy`` decodes it
     again). To capture a backward pass into a CUDA graph, capture
@@ -609,6 +621,7 @@ class TiledWeights:
         is): an x that asks for a gradient is refused."""
         import torch
         act_id = _act_id(act)
+        _refuse_tangents(x)
         if x.requires_grad and torch.is_grad_enabled():
             raise ValueError("no gradient passes through TiledWeights.gated (give x.detach(), or use ResidentModel.gated)")
         if self.shapes[gate] != self.shapes[up]:
@@ -822,6 +835,7 @@ class ResidentModel:
         if route not in ("auto", "fused", "decode"):
             raise ValueError(f"unknown route {route!r}")
         _act_id(act)
+        _refuse_tangents(x)
         (rows, cols), other = self._matrices(layer, (gate, up))[2]
         if (rows, cols) != other:
             raise ValueError(f"expected two matrices of one shape, got {(rows, cols)}, {other}")
@@ -847,6 +861,7 @@ class ResidentModel:
         if x.device != self.layers[layer]["blobs"][index].device:
             raise ValueError("x must be on the matrix's device")
         _check_targets(x, targets, reduction)
+        _refuse_tangents(x)
         if x.requires_grad and torch.is_grad_enabled():
             with _On(x.device, stream, (x, targets, status)):
                 return _functions()["resident_xent"].apply(x, self, layer, index, targets, ignore_index, reduction,

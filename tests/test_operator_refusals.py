@@ -228,3 +228,30 @@ def test_xent_backward_from_losses():
     refused(lwc.LWC_ERR_MISALIGNED, back, x, P, P, P, 0, True, P + 1, P, P, 1 << 30)
     refused(lwc.LWC_ERR_MISALIGNED, back, x, P, P, P, 0, True, P, P, P + 16, 1 << 30)
     back(x, P, None, P, 0, True, None, None, None, 0)
+
+
+def test_forward_mode_is_refused():
+    """A dual tensor asks for no gradient, so its tangent would be dropped silently."""
+    torch = pytest.importorskip("torch")
+    from torch.autograd import forward_ad
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(128, 64, dtype=torch.bfloat16)
+    t, f = torch.zeros(2, dtype=torch.int64), torch.zeros(2)
+    h = torch.zeros(2, 128, dtype=torch.bfloat16)
+    model = layers.ResidentModel("codebook", "cpu")
+    model.layers.append(dict(descs=[lwc.lwc_desc()] * 2, blobs=[torch.zeros(1)] * 2, shapes=[(128, 64)] * 2))
+    tw = layers.TiledWeights("cpu")
+    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc(), lwc.lwc_desc()], [None, None], [(128, 64), (128, 64)]
+    with forward_ad.dual_level():
+        def dual(v):
+            return forward_ad.make_dual(v, torch.ones_like(v))
+        for call in (lambda: layers.gated_ffn(dual(x), w, w), lambda: layers.gated_ffn(x, w, dual(w)),
+                     lambda: layers.gated_ffn_backward(dual(h), x, w, w),
+                     lambda: layers.linear_cross_entropy(dual(x), w, t), lambda: layers.linear_cross_entropy(x, dual(w), t),
+                     lambda: layers.linear_cross_entropy_backward(dual(f), f, x, w, t, reduction="none"),
+                     lambda: model.gated(0, 0, 1, dual(x)), lambda: model.cross_entropy(0, 0, dual(x), t),
+                     lambda: tw.gated(0, 1, dual(x))):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+        # plain tensors meet their own checks inside a dual level too
+        with pytest.raises(ValueError, match="CUDA"):
+            layers.gated_ffn(x, w, w)
