@@ -52,8 +52,8 @@ __device__ __forceinline__ float activation(uint32_t act, float v, float &slope)
             return v * c;
         }
         case LWC_ACT_GELU_TANH: {
-            // 0.5 (1 + tanh q) = sigmoid(2 q)
-            const float v2 = v * v, q2 = 2.0f * kGeluC * v * (1.0f + kGeluA * v2), p = sigmoid(q2);
+            // 0.5 (1 + tanh q) = sigmoid(2 q); beyond |v| = 10^4 p is 0 or 1 anyway, but v^2 may be infinite
+            const float v2 = fminf(v * v, 1e8f), q2 = 2.0f * kGeluC * v * (1.0f + kGeluA * v2), p = sigmoid(q2);
             if (kSlope) slope = p + v * p * (1.0f - p) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * v2);
             return v * p;
         }

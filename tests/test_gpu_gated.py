@@ -566,3 +566,24 @@ def test_resident_model_of_other_blocks(M):
     assert torch.equal(xg.grad, layers.gated_ffn_backward(torch.ones_like(h), x, wg, wu, need=(True, False, False))[0])
     with pytest.raises(lwc.LwcError, match="blocks of 32 chunks"):
         model.gated(0, 0, 1, x, route="fused")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu", "sigmoid"])
+def test_arguments_whose_powers_overflow(act):
+    """|a| up to 1e38: a^2 and a^3 are beyond FP32, the activation and its slope are not."""
+    K = 16
+    a = torch.tensor([1e4, 1e7, 1e13, 3e18, 1e20, 1e30, 1e38], device="cuda")
+    a = torch.cat([a, -a, a.new_zeros(2)]).bfloat16()
+    M = a.numel()
+    x = torch.zeros(M, K, device="cuda").bfloat16()
+    x[:, 0], x[:, 1] = a, 1.0
+    wg, wu = (torch.zeros(8, K, device="cuda").bfloat16() for _ in range(2))
+    wg[:, 0], wu[:, 1] = 1.0, 2.0 ** -6     # a and b = 2^-6, exact
+    dh = torch.ones(M, 8, device="cuda").bfloat16()
+    y, s = act64(act, a.double())
+    h = layers.gated_ffn(x, wg, wu, act=act)
+    # |v| is 0 or so large that the activation is v, 1 or 0; h is rounded once
+    close(h, (y / 64)[:, None].expand(M, 8), (2.0 ** -8 * (y / 64).abs() + 1e-30)[:, None].expand(M, 8))
+    dx = layers.gated_ffn_backward(dh, x, wg, wu, act=act, need=(True, False, False))[0]
+    want = 8 * s / 64      # eight features alike
+    close(dx[:, 0], want, 2 * 2.0 ** -8 * want.abs() + 1e-30)
