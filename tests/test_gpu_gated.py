@@ -500,16 +500,19 @@ def test_tiled_weights_on_another_stream():
 
 def late(stream, call, *tensors):
     """call(*copies of tensors) on `stream` behind some 100 ms of other work, where the copies are freed, and
-    their memory written again, long before the call's kernels run."""
-    copies = [t.clone().requires_grad_(t.requires_grad) for t in tensors]
-    stream.wait_stream(torch.cuda.current_stream())
-    with torch.cuda.stream(stream):
-        torch.cuda._sleep(200_000_000)
-    result = call(*copies).detach()
-    del copies
-    junk = [torch.full_like(t, 7) for t in tensors for _ in range(2)]
-    assert not stream.query(), "the work ahead of the call ended too early to show anything"
-    torch.cuda.synchronize()
+    their memory written again, long before the call's kernels run. Once without that work first: loading a
+    kernel may wait for the device."""
+    for cycles in (1000, 200_000_000):
+        copies = [t.clone().requires_grad_(t.requires_grad) for t in tensors]
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(cycles)
+        result = call(*copies).detach()
+        del copies
+        junk = [torch.full_like(t, 7) for t in tensors for _ in range(2)]
+        behind = not stream.query()
+        torch.cuda.synchronize()
+    assert behind, "the work ahead of the call ended too early to show anything"
     return result, junk
 
 
