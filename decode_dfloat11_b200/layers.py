@@ -613,10 +613,17 @@ class TiledWeights:
         fn(batch, d_status=status, stream=stream)
         return outs
 
+    def _one_launch(self, a: int, b: int) -> bool:
+        """Whether two matrices of one shape fit a batched call: one index width (codebook; two matrices' distinct
+        values may lie on either side of a power of two) or chunk size (DFloat11), at most 4096 units of 128 rows."""
+        alike = "k" if self.codec == "codebook" else "chunk_bytes"
+        return getattr(self.descs[a], alike) == getattr(self.descs[b], alike) and \
+            2 * self.shapes[a][0] <= 128 * 4096
+
     def gated(self, gate: int, up: int, x, act: str = "silu", out=None, stream=None, status=None):
         """h = act(x W_gate^T) * (x W_up^T) for two matrices of one shape, held
-        in tile order: both products in one launch (x: M x cols BF16, M <=
-        256), then the activation and the product. Returns ``out`` (M x rows
+        in tile order: both products in one launch where it takes them together
+        (x: M x cols BF16, M <= 256), then the activation and the product. Returns ``out`` (M x rows
         BF16, allocated if None). Not differentiable (``ResidentModel.gated``
         is): an x that asks for a gradient is refused."""
         import torch
@@ -638,7 +645,11 @@ class TiledWeights:
             else:
                 _check_out(out, (M, rows), x)
             ab = torch.empty((2, M, rows), dtype=torch.float32, device=x.device)
-            self.gemm_batched([gate, up], [x, x], [ab[0], ab[1]], stream=s, status=status)
+            if self._one_launch(gate, up):
+                self.gemm_batched([gate, up], [x, x], [ab[0], ab[1]], stream=s, status=status)
+            else:
+                for index, y in zip((gate, up), ab):
+                    self.gemm(index, x, y, stream=s, status=status)
             lwc.lwc_gated_product(lwc.LWC_ELEM_BF16, act_id, ab[0], ab[1], M * rows, out, s)
         return out
 

@@ -590,3 +590,22 @@ def test_arguments_whose_powers_overflow(act):
     dx = layers.gated_ffn_backward(dh, x, wg, wu, act=act, need=(True, False, False))[0]
     want = 8 * s / 64      # eight features alike
     close(dx[:, 0], want, 2 * 2.0 ** -8 * want.abs() + 1e-30)
+
+
+@pytest.mark.parametrize("codec", layers.CODECS)
+def test_tiled_weights_of_unlike_blobs(codec):
+    """Two matrices that one launch does not take together: another index width, another chunk size."""
+    N, K, M = 256, 192, 40
+    wg, wu = (synth.normal_bf16((N, K), seed=s, sigma=0.05, outlier_frac=1e-3, device="cuda") for s in (3, 4))
+    if codec == "codebook":
+        wu = (wu * 64).round().clamp(-8, 8).div(64).bfloat16()   # a handful of values
+    tw = layers.TiledWeights("cuda", codec)
+    gate, up = tw.add(wg), tw.add(wu, **({} if codec == "codebook" else {"chunk_bytes": 36}))
+    assert (tw.descs[gate].k, tw.descs[gate].chunk_bytes) != (tw.descs[up].k, tw.descs[up].chunk_bytes)
+    x = torch.randn(M, K, generator=torch.Generator("cuda").manual_seed(M), device="cuda").bfloat16()
+    e = Exact("silu", x, wg, wu)
+    close(tw.gated(gate, up, x), e.h, e.h_tol)
+    e = Exact("silu", x, wu, wg)
+    close(tw.gated(up, gate, x), e.h, e.h_tol)
+    e = Exact("silu", x, wg, wg)
+    close(tw.gated(gate, gate, x), e.h, e.h_tol)   # one matrix twice

@@ -255,3 +255,24 @@ def test_forward_mode_is_refused():
         # plain tensors meet their own checks inside a dual level too
         with pytest.raises(ValueError, match="CUDA"):
             layers.gated_ffn(x, w, w)
+
+
+@pytest.mark.parametrize("codec,one,other", [("codebook", dict(k=12), dict(k=13)),
+                                             ("dfloat11", dict(chunk_bytes=20), dict(chunk_bytes=36))])
+def test_tiled_matrices_that_one_launch_does_not_take(monkeypatch, codec, one, other):
+    torch = pytest.importorskip("torch")
+    calls = []
+    for name in (f"lwc_gemm_{codec}", f"lwc_gemm_{codec}_batched"):
+        monkeypatch.setattr(lwc, name, lambda *args, name=name, **kwargs: calls.append(name))
+    monkeypatch.setattr(lwc, "lwc_gated_product", lambda *args: None)
+    monkeypatch.setattr(layers, "_On", lambda *args: contextlib.nullcontext())
+    tw = layers.TiledWeights("cpu", codec)
+    tw.descs = [lwc.lwc_desc(**one), lwc.lwc_desc(**one), lwc.lwc_desc(**other)]
+    tw.blobs, tw.shapes = [None] * 3, [(128, 64)] * 3
+    for up, want in ((1, [f"lwc_gemm_{codec}_batched"]), (2, [f"lwc_gemm_{codec}"] * 2)):
+        calls.clear()
+        tw.gated(0, up, torch.zeros(2, 64, dtype=torch.bfloat16))
+        assert calls == want
+    for rows, together in ((128 * 2048, True), (128 * 2049, False)):
+        tw.shapes = [(rows, 64)] * 3
+        assert tw._one_launch(0, 1) == together
