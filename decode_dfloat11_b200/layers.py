@@ -110,11 +110,11 @@ def fused_linear(desc, blob, shape, x, codec: str, out=None, stream=None, status
     if route == "auto":
         route = "decode" if codec == "dfloat11" and M > DF11_FUSED_MAX_M else "fused"
     if route == "decode":
-        s = stream if stream is not None else torch.cuda.current_stream(x.device)
-        w = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
         dec = lwc.lwc_decode_dfloat11_checked if codec == "dfloat11" else lwc.lwc_decode_codebook_checked
-        dec(desc, blob, w, status, s)
-        with torch.cuda.stream(s):
+        with _On(x.device, stream, (x, out, status)) as s:
+            # the buffer belongs to the stream that still uses it when this returns
+            w = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+            dec(desc, blob, w, status, s)
             out.copy_(torch.mm(x, w.t(), out_dtype=torch.float32))
         return out
     fn = lwc.lwc_linear_dfloat11 if codec == "dfloat11" else lwc.lwc_linear_codebook

@@ -132,3 +132,24 @@ def test_outputs_and_status_words_are_recorded_too(recorder, tiled, monkeypatch,
     used = [u for stream, given in recorder.given if stream == STREAM for u in given]
     assert any(u is status for u in used)
     assert any(u is out for u in used) or call.startswith("linear")
+
+
+@pytest.mark.parametrize("codec", layers.CODECS)
+def test_a_decoded_buffer_belongs_to_the_stream_that_uses_it(recorder, monkeypatch, codec):
+    """fused_linear's route "decode" returns before its buffer has been read."""
+    where = []
+    plain = torch.empty
+
+    def empty(shape, **kwargs):
+        if tuple(shape) == (16, 64):
+            where.append(list(Recorder.inside))
+        return plain(shape, **kwargs)
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch, "mm", lambda x, w, out_dtype: plain((x.shape[0], w.shape[1]), dtype=out_dtype).zero_())
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: layers.contextlib.nullcontext())
+    for name in ("lwc_decode_dfloat11_checked", "lwc_decode_codebook_checked"):
+        monkeypatch.setattr(lwc, name, lambda *args: None)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    layers.fused_linear(lwc.lwc_desc(), None, (16, 64), x, codec, stream=STREAM, route="decode")
+    assert where == [[STREAM]]
