@@ -218,12 +218,12 @@ lwc_status marshal_product(const Product &p, TcArgs &P, uint32_t &grid, uint32_t
     // m tiles walked together: all of them where A stays in L2 while B, which does
     // not, is read once (4096 tokens' losses over 128256 words, 33 MB of A in 16 m
     // tiles: 3.89, 3.60, 3.52, 3.42, 3.42 and 3.37 ms for groups of 2, 4, 6, 8, 12 and
-    // 16), but for the gated product, which also writes, no more than 12 (4096 x
-    // 14336 x 4096: 727, 723, 706, 694, 687 and 741 us); else as many as make the tiles
-    // that run at a time about square.
+    // 16; the gated product of 13, 16, 20 and 24 m tiles by 14336 x 4096 takes the same
+    // time, within 1 %, for 7, 8, 10, 12 and all); else as many as make the tiles that
+    // run at a time about square.
     const uint64_t a_bytes = 2 * p.m * (p.k + p.k2), b_bytes = 2 * p.n * (p.k + p.k2) * (halves ? 2 : 1);
     const bool resident = a_bytes <= kResidentBytes && b_bytes > kResidentBytes;
-    P.group = std::min<uint32_t>(P.m_tiles, !resident ? 8 : halves ? 12 : P.m_tiles);
+    P.group = resident ? P.m_tiles : std::min<uint32_t>(P.m_tiles, 8);
     P.whole = (uint32_t)p.whole;
     P.units = P.whole + (P.m_tiles * P.n_tiles * p.batch - P.whole) * p.splits;
     P.stage_bytes = kABytes + w * 128u;
