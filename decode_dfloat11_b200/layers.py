@@ -156,7 +156,8 @@ def _check_matrices(x, **matrices):
 def _refuse_tangents(*tensors):
     """Forward-mode differentiation does not pass through the kernels: a dual
     tensor's tangent would be dropped without a word."""
-    from torch.autograd import forward_ad
+    import torch
+    forward_ad = torch.autograd.forward_ad
     if forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors):
         raise NotImplementedError("the operator has no forward-mode derivative (a dual tensor was given)")
 
