@@ -635,6 +635,8 @@ class TiledWeights:
         if self.shapes[gate] != self.shapes[up]:
             raise ValueError(f"matrices differ in shape: {self.shapes[gate]}, {self.shapes[up]}")
         rows, _ = self._check_x(gate, x)
+        if any(x.device != self.blobs[i].device for i in (gate, up)):
+            raise ValueError("x must be on the matrices' device")
         M = int(x.shape[0])
         with _On(x.device, stream, (x, out, status)) as s:
             # laid out on the stream that reads it

@@ -153,7 +153,7 @@ def test_a_product_without_a_gradient_refuses_to_drop_one(monkeypatch):
     """TiledWeights.gated has no backward pass: its result would silently end the graph."""
     torch = pytest.importorskip("torch")
     tw = layers.TiledWeights("cpu")
-    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc(), lwc.lwc_desc()], [None, None], [(128, 64), (128, 64)]
+    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc(), lwc.lwc_desc()], [torch.zeros(1)] * 2, [(128, 64), (128, 64)]
     x = torch.zeros(2, 64, dtype=torch.bfloat16, requires_grad=True)
     with pytest.raises(ValueError, match="gradient"):
         tw.gated(0, 1, x)
@@ -240,7 +240,7 @@ def test_forward_mode_is_refused():
     model = layers.ResidentModel("codebook", "cpu")
     model.layers.append(dict(descs=[lwc.lwc_desc()] * 2, blobs=[torch.zeros(1)] * 2, shapes=[(128, 64)] * 2))
     tw = layers.TiledWeights("cpu")
-    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc(), lwc.lwc_desc()], [None, None], [(128, 64), (128, 64)]
+    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc(), lwc.lwc_desc()], [torch.zeros(1)] * 2, [(128, 64), (128, 64)]
     with forward_ad.dual_level():
         def dual(v):
             return forward_ad.make_dual(v, torch.ones_like(v))
@@ -268,7 +268,7 @@ def test_tiled_matrices_that_one_launch_does_not_take(monkeypatch, codec, one, o
     monkeypatch.setattr(layers, "_On", lambda *args: contextlib.nullcontext())
     tw = layers.TiledWeights("cpu", codec)
     tw.descs = [lwc.lwc_desc(**one), lwc.lwc_desc(**one), lwc.lwc_desc(**other)]
-    tw.blobs, tw.shapes = [None] * 3, [(128, 64)] * 3
+    tw.blobs, tw.shapes = [torch.zeros(1)] * 3, [(128, 64)] * 3
     for up, want in ((1, [f"lwc_gemm_{codec}_batched"]), (2, [f"lwc_gemm_{codec}"] * 2)):
         calls.clear()
         tw.gated(0, up, torch.zeros(2, 64, dtype=torch.bfloat16))
@@ -276,3 +276,12 @@ def test_tiled_matrices_that_one_launch_does_not_take(monkeypatch, codec, one, o
     for rows, together in ((128 * 2048, True), (128 * 2049, False)):
         tw.shapes = [(rows, 64)] * 3
         assert tw._one_launch(0, 1) == together
+
+
+def test_tiled_matrices_of_another_device_are_refused(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(lwc, "lwc_gemm_dfloat11_batched", lambda *args, **kwargs: pytest.fail("launched"))
+    tw = layers.TiledWeights("meta")
+    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc()] * 2, [torch.zeros(1, device="meta")] * 2, [(128, 64)] * 2
+    with pytest.raises(ValueError, match="device"):
+        tw.gated(0, 1, torch.zeros(2, 64, dtype=torch.bfloat16))

@@ -49,7 +49,7 @@ def tiled(monkeypatch):
     for name in ("lwc_gemm_dfloat11", "lwc_gemm_dfloat11_batched", "lwc_gated_product", "lwc_linear_dfloat11"):
         monkeypatch.setattr(lwc, name, lambda *args, **kwargs: None)
     tw = layers.TiledWeights("cpu")
-    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc(), lwc.lwc_desc()], [None, None], [(128, 64), (128, 64)]
+    tw.descs, tw.blobs, tw.shapes = [lwc.lwc_desc(), lwc.lwc_desc()], [torch.zeros(1)] * 2, [(128, 64), (128, 64)]
     return tw
 
 
