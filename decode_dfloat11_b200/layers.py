@@ -196,6 +196,8 @@ class _On:
             return torch._C._cuda_getCurrentRawStream(self.device.index)
         if isinstance(self.stream, int):   # a raw handle, as the C calls take
             self.stream = torch.cuda.ExternalStream(self.stream, device=self.device)
+        if self.stream is not None and self.stream.device != self.device:
+            raise ValueError(f"the stream is of {self.stream.device}, the tensors are on {self.device}")
         self.stack = contextlib.ExitStack()
         self.stack.enter_context(torch.cuda.device(self.device))
         current = torch.cuda.current_stream(self.device)

@@ -153,3 +153,12 @@ def test_a_decoded_buffer_belongs_to_the_stream_that_uses_it(recorder, monkeypat
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     layers.fused_linear(lwc.lwc_desc(), None, (16, 64), x, codec, stream=STREAM, route="decode")
     assert where == [[STREAM]]
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda:1")
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        with layers._On(torch.device("cuda:0"), Stream()):
+            pytest.fail("entered")
