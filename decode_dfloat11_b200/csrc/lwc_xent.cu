@@ -34,7 +34,7 @@ namespace {
 using tc::Product;
 
 constexpr float kLog2e = 1.4426950408889634f;
-// P in FP16 is scaled by this power of two: |P| <= 1 before, so nothing
+// P in FP16 is scaled by this power of two: |P| <= 1 before (but for roundings), so nothing
 // overflows, and a probability is kept to full precision down to 4e-9 (without
 // it a uniform distribution over 128256 words would be subnormal).
 constexpr float kFp16Scale = 16384.0f;
@@ -281,31 +281,36 @@ __global__ void xent_total_kernel(const float *__restrict__ loss, const int64_t 
     }
 }
 
-// coef_i = c_i / max |c| (times kFp16Scale for FP16), alpha = max |c| (over it):
-// P has the scale of the probabilities whatever the loss is divided by, and
-// where every token counts alike, coef is 1, so that the largest entry of a
-// row, p - 1 at the target, is not rounded by a factor that all rows share.
-// The maximum is of the finite |c|: an infinite or NaN gradient spoils its own
-// token's row of dx (and dW), not the scale of the others.
-// FP16: a token whose |c| is below 2^-12 of the largest has probabilities below
-// 2^-16 among FP16's subnormal numbers (a step of 2^-38 of the largest |c|).
+// coef_i = c_i / unit (times kFp16Scale for FP16), alpha = unit (over it), with
+// unit the largest entry of c P, c_i (1 - p_i) of one of the targets: P lies in
+// [-1, 1] whatever the loss is divided by and however sure the tokens are, and
+// the entry that weighs most, alone where there is one token, is not rounded
+// (scaled by max |c| instead, one token's gradients were off by up to 2^-8 as a
+// whole). At least 2^-64 of max |c|, so that coef stays finite.
+// Only finite values count: an infinite or NaN gradient spoils its own token's
+// row of dx (and dW), not the scale of the others.
+// FP16: entries below 2^-28 of the largest are subnormal numbers (steps of
+// 2^-38 of it): those of a token whose |c| is small, or whose tail is thin.
 // One block.
 __global__ void xent_coef_kernel(const float *__restrict__ grad, uint64_t grad_stride,
-                                 const int64_t *__restrict__ targets, int64_t ignore, uint64_t rows, uint64_t vocab,
-                                 uint32_t mean, uint32_t fp16, float *__restrict__ coef, float *__restrict__ alpha) {
-    __shared__ float tops[32];
+                                 const float *__restrict__ loss, const int64_t *__restrict__ targets, int64_t ignore,
+                                 uint64_t rows, uint64_t vocab, uint32_t mean, uint32_t fp16, float *__restrict__ coef,
+                                 float *__restrict__ alpha) {
+    __shared__ float2 tops[32];
     __shared__ unsigned long long counts[32];
     tc::wait_for_stream();
-    float top = 0.0f;
+    float2 top = {0.0f, 0.0f};   // of |c|, of the targets' entries
     unsigned long long n = 0;
     for (uint64_t i = threadIdx.x; i < rows; i += blockDim.x) {
         const int64_t t = target_of(targets[i], ignore, vocab);
         n += t != -1;
-        const float g = t >= 0 ? fabsf(grad[i * grad_stride]) : 0.0f;
-        if (isfinite(g)) top = fmaxf(top, g);
+        const float c = t >= 0 ? fabsf(grad[i * grad_stride]) : 0.0f, e = t >= 0 ? -expm1f(-loss[i]) * c : 0.0f;
+        if (isfinite(c)) top.x = fmaxf(top.x, c);
+        if (isfinite(e)) top.y = fmaxf(top.y, e);
     }
     for (uint32_t d = 16; d; d >>= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        top.x = fmaxf(top.x, __shfl_xor_sync(0xFFFFFFFFu, top.x, d));
+        top.y = fmaxf(top.y, __shfl_xor_sync(0xFFFFFFFFu, top.y, d));
         n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
     }
     if ((threadIdx.x & 31u) == 0) {
@@ -313,14 +318,15 @@ __global__ void xent_coef_kernel(const float *__restrict__ grad, uint64_t grad_s
         counts[threadIdx.x >> 5] = n;
     }
     __syncthreads();
-    top = 0.0f;
+    top = make_float2(0.0f, 0.0f);
     n = 0;
     for (uint32_t w = 0; w < blockDim.x >> 5; w++) {
-        top = fmaxf(top, tops[w]);
+        top.x = fmaxf(top.x, tops[w].x);
+        top.y = fmaxf(top.y, tops[w].y);
         n += counts[w];
     }
     const float div = mean ? (float)(n ? n : 1) : 1.0f;
-    const float c = top / div, unit = c > 0.0f ? c : 1.0f;
+    const float most = fmaxf(top.y, top.x * 0x1p-64f) / div, unit = most > 0.0f ? most : 1.0f;
     const float scale = fp16 ? kFp16Scale : 1.0f;
     for (uint64_t i = threadIdx.x; i < rows; i += blockDim.x) {
         const bool on = target_of(targets[i], ignore, vocab) >= 0;
@@ -581,8 +587,9 @@ lwc_status backward(const lwc_xent *x, const float *d_lse, const float *d_loss, 
         d_loss = loss;
     }
     st = launched("loss coefficients",
-                  tc::launch_next(xent_coef_kernel, dim3(1), 1024, 0, 1, s, d_grad, grad_stride, x->targets,
-                                  x->ignore_index, x->tokens, x->vocab, (uint32_t)(mean != 0), fp16, coef, alpha));
+                  tc::launch_next(xent_coef_kernel, dim3(1), 1024, 0, 1, s, d_grad, grad_stride, d_loss,
+                                  x->targets, x->ignore_index, x->tokens, x->vocab, (uint32_t)(mean != 0), fp16, coef,
+                                  alpha));
     if (!st && d_dhead) st = tc::launch_transpose(x->x, x->ld_x, x->tokens, x->hidden, coef, xt, s);
     for (uint64_t first = 0; first < x->vocab && !st; first += b.piece) {
         const uint64_t width = std::min(b.piece, x->vocab - first);

@@ -450,8 +450,8 @@ LWC_API lwc_status lwc_xent_forward(const lwc_xent *x, float *d_loss, float *d_l
  *     dx = P head,  dhead = P^T x
  * into contiguous matrices of type `elem`; either may be NULL. The logits are
  * computed again, a piece of the vocabulary at a time; P is rounded to `elem`
- * once, divided by the largest finite |c_i| (and, for FP16, times 2^14, so that
- * small probabilities keep their digits: entries below 2^-28 of that |c_i| are
+ * once, divided by its largest finite entry (and, for FP16, times 2^14, so that
+ * small probabilities keep their digits: entries below 2^-28 of the largest are
  * subnormal numbers, in steps of 2^-38); sums are FP32. An infinite or NaN c_i
  * spoils dhead and its own row of dx only. Repeats bit for bit. d_lse:
  * lwc_xent_forward's, for the same x. With tokens = 0, dhead is zeros. */

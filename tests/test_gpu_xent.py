@@ -568,3 +568,42 @@ def test_an_infinite_gradient_stays_in_its_row(bad, dtype):
     for reduction in ("sum", "mean"):
         dx, _ = layers.linear_cross_entropy_backward(torch.tensor(bad, device="cuda"), lse, x, w, t, reduction=reduction)
         assert not dx[t == IGNORE].any() and not bool(dx[t != IGNORE].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("V", [2, 500])
+def test_the_entry_that_weighs_most_is_not_rounded(V, dtype):
+    """One token: its target's row of dW is -(1 - p) c x, rounded once: P's scale is its largest entry."""
+    K = 256
+    g = torch.Generator("cuda").manual_seed(27)
+    w = torch.randn(V, K, generator=g, device="cuda").mul_(K ** -0.5).to(dtype)
+    for k, lean in enumerate(torch.linspace(0.0, 6.0, 12).tolist()):
+        t = torch.tensor([k % V], device="cuda")
+        x = (torch.randn(1, K, generator=g, device="cuda") + lean * w[t].float()).to(dtype)
+        c = torch.tensor([0.37 + 0.11 * k], device="cuda")
+        q, _, _ = confident_bound(x, w, t, float(c))
+        # the logits' differences, then expm1, log1p and the scale in FP32
+        rel = 2 * (gamma(256) + 16 * U) * float((x.double().abs() @ w.double().abs().T).max()) + 2.0 ** -18
+        loss, lse = layers.linear_cross_entropy(x, w, t, reduction="none", return_lse=True)
+        _, dw = layers.linear_cross_entropy_backward(c, lse, x, w, t, reduction="none", loss=loss)
+        want = -q[:, None] * c.double() * x.double()
+        close(dw[t], want, (HALF[dtype] * (1 + rel) + rel) * want.abs() + TINY[dtype])
+
+
+def test_the_scale_of_p_stays_finite():
+    """Tokens so sure that no entry of P is left (1 - p below 1e-38), alone and beside another one."""
+    x, w, t = inputs(3, 40, 64, torch.bfloat16, seed=28, ignored=0.0)
+    t[1] = t[2] = t[0]
+    x[0] = x[1] = (200 * w[t[0]].float()).bfloat16()
+    for rows in (slice(0, 1), slice(0, 2), slice(0, 3)):
+        for dtype in TYPES:
+            leaves = [v.detach().clone().to(dtype).requires_grad_() for v in (x[rows], w)]
+            loss = layers.linear_cross_entropy(*leaves, t[rows], reduction="sum")
+            loss.backward()
+            ref = [v.detach().double().requires_grad_() for v in leaves]
+            want = torch.nn.functional.cross_entropy(ref[0] @ ref[1].T, t[rows], reduction="sum")
+            want.backward()
+            for v, r in zip(leaves, ref):
+                assert bool(v.grad.isfinite().all())
+                # the third token's share is all there is: a chain of three roundings
+                assert float((v.grad.double() - r.grad).norm()) <= 3 * HALF[dtype] * float(r.grad.norm()) + 1e-12
