@@ -607,3 +607,54 @@ def test_the_scale_of_p_stays_finite():
                 assert bool(v.grad.isfinite().all())
                 # the third token's share is all there is: a chain of three roundings
                 assert float((v.grad.double() - r.grad).norm()) <= 3 * HALF[dtype] * float(r.grad.norm()) + 1e-12
+
+
+def test_no_tokens_and_a_padded_batch_through_autograd():
+    x, w, t = inputs(24, 70, 32, torch.bfloat16, seed=29, ignored=0.0)
+    for reduction in ("none", "mean", "sum"):
+        leaves = [x[:0].clone().requires_grad_(), w.clone().requires_grad_()]
+        layers.linear_cross_entropy(*leaves, t[:0], reduction=reduction).sum().backward()
+        assert leaves[0].grad.shape == (0, 32) and not leaves[1].grad.any()
+    # sequences of 8, 3 and 0 tokens padded to 8: the same as their tokens alone
+    keep = torch.arange(8, device="cuda") < torch.tensor([[8], [3], [0]], device="cuda")
+    pad = torch.where(keep.view(-1, 1), x, float("nan")).view(3, 8, 32)
+    one = [pad.clone().requires_grad_(), w.clone().requires_grad_()]
+    two = [x[keep.view(-1)].clone().requires_grad_(), w.clone().requires_grad_()]
+    a = layers.linear_cross_entropy(*one, torch.where(keep, t.view(3, 8), IGNORE))
+    b = layers.linear_cross_entropy(*two, t[keep.view(-1)])
+    assert abs(float(a.detach()) - float(b.detach())) <= 2.0 ** -20 * float(b.detach())
+    a.backward()
+    b.backward()
+    assert not one[0].grad[~keep].any()
+    # the same entries, but in another place of the contraction over tokens
+    e = Exact(two[0].detach(), w, t[keep.view(-1)], torch.full((11,), 1 / 11, device="cuda"))
+    close(one[0].grad[keep], e.dx, e.dx_tol)
+    close(one[1].grad, e.dw, e.dw_tol)
+
+
+def test_two_graphs_replayed_in_turn():
+    """Each with its own workspace: a step of one between two of the other changes nothing."""
+    graphs, outs, wants = [], [], []
+    grad = torch.ones((), device="cuda")
+    for seed in (30, 31):
+        x, w, t = inputs(300, 600, 128, torch.bfloat16, seed=seed)
+        losses, lse = layers.linear_cross_entropy(x, w, t, reduction="none", return_lse=True)
+        wants.append((losses, *layers.linear_cross_entropy_backward(grad, lse, x, w, t)))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            losses, lse = layers.linear_cross_entropy(x, w, t, reduction="none", return_lse=True)
+            given = layers.linear_cross_entropy_backward(grad, lse, x, w, t, loss=losses)
+            again = layers.linear_cross_entropy_backward(grad, lse, x, w, t)
+        graphs.append((graph, x, w, t))
+        outs.append((losses, *given, *again))
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        side.wait_stream(torch.cuda.current_stream())
+        graphs[0][0].replay()
+        with torch.cuda.stream(side):
+            graphs[1][0].replay()
+        torch.cuda.synchronize()
+        for got, want in zip(outs, wants):
+            assert torch.equal(got[0], want[0])
+            assert all(torch.equal(g, r) for g, r in zip(got[1:], (*want[1:], *want[1:])))
