@@ -217,7 +217,7 @@ lwc_status marshal_product(const Product &p, TcArgs &P, uint32_t &grid, uint32_t
     P.chunk = p.chunk ? p.chunk : P.steps;
     // m tiles walked together: all of them where A stays in L2 while B, which does
     // not, is read once (4096 tokens' losses over 128256 words, 33 MB of A in 16 m
-    // tiles: 3.89, 3.60, 3.52, 3.42, 3.42 and 3.37 ms for groups of 2, 4, 6, 8, 12 and
+    // tiles: 3.72, 3.55, 3.54, 3.59, 3.62 and 3.40 ms for groups of 2, 4, 6, 8, 12 and
     // 16; the gated product of 13, 16, 20 and 24 m tiles by 14336 x 4096 takes the same
     // time, within 1 %, for 7, 8, 10, 12 and all); else as many as make the tiles that
     // run at a time about square.

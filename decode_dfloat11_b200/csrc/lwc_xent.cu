@@ -39,8 +39,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // it a uniform distribution over 128256 words would be subnormal).
 constexpr float kFp16Scale = 16384.0f;
 // Bytes of P per piece of the vocabulary. Gradients of 4096 tokens x 128256 words
-// x 4096: 10.9, 9.9, 10.0, 9.7 and 9.7 ms for 48, 96, 192, 384 and 800 MB (each piece
-// adds to dx in 32 bits and ends in incomplete waves of tiles).
+// x 4096: 11.7, 10.9, 10.4, 10.1 and 10.0 ms for 48, 96, 192, 384 and 800 MB (each
+// piece adds to dx in 32 bits and ends in incomplete waves of tiles).
 constexpr uint64_t kPieceBytes = 384ull << 20;
 
 // 2^v, off by at most 2^-22 of it; 0 below 2^-126.
@@ -60,9 +60,10 @@ __device__ __forceinline__ int64_t target_of(int64_t t, int64_t ignore, uint64_t
 // zero, so a long sum drifts: 3e-6 of the loss at K = 4096. The logits are
 // therefore summed a chunk of 64-term steps at a time and the parts added,
 // rounded, in registers (16 columns of 8 chunks a thread). 8 steps leave
-// 3.5e-7; 4 steps would leave half of it, but cost an eighth of the time
-// where the products bound it (2048 tokens x 128256 words: 2.07 ms, not 1.85),
-// and nothing for few rows, where W's way from memory does.
+// 3.5e-7; 4 steps would leave two thirds of it, but take 2.26 ms instead of 1.55
+// where the products bound the time (2048 tokens x 128256 words; 1.36 in one
+// run, with eight times the error), and nothing for few rows, where W's way from
+// memory does. Backward, 4096 tokens: 10.9, 9.65 and 9.46 ms for 4, 8 and one run.
 constexpr uint32_t kChunkSteps = 8, kChunkStepsFewRows = 4;
 uint32_t chunk_steps(uint64_t tokens) { return tokens > tc::kRows ? kChunkSteps : kChunkStepsFewRows; }
 

@@ -385,8 +385,9 @@ typedef struct lwc_gated {
 } lwc_gated;
 
 /* h, rows ld_h elements apart (at least features; 2-byte aligned, written
- * with 16-byte stores where base and rows are 16-byte aligned). One kernel on
- * the tensor cores (tcgen05, sm_100 only); products are exact, sums,
+ * with 16-byte stores where base and rows are 16-byte aligned). One kernel
+ * (sm_100 only) on the tensor cores (tcgen05), or, for one row and for up to
+ * four of small matrices, on the FP32 units; products are exact, sums,
  * activation and product FP32 (sums as stated for lwc_gemm_dfloat11), rounded
  * once, to nearest. Repeats bit for bit. Nothing but h is written. d_status:
  * optional; LWC_DEVICE_TIMEOUT is OR-ed in if a bounded wait gave up (h is
