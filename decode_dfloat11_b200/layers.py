@@ -297,13 +297,13 @@ def gated_ffn(x, w_gate, w_up, act: str = "silu", out=None, stream=None, status=
     the caller orders it after what makes the inputs). ``status``: optional
     device status word.
 
-    Differentiable for x, w_gate and w_up (once, in reverse mode); the two projections are not
-    kept but computed again in the backward pass, so the matrices must still
-    hold the same values there. Matrices decoded into a reused buffer do not:
-    use ``ResidentModel.gated``, which decodes them again. To capture a backward
-    pass into a CUDA graph, capture ``gated_ffn_backward``: autograd's own joins
-    the streams of other graphs of the same leaves that are still alive, which a
-    capture forbids."""
+    Differentiable for x, w_gate and w_up (once, in reverse mode); the two
+    projections are not kept but computed again in the backward pass, so the
+    matrices must still hold the same values there. Matrices decoded into a
+    reused buffer do not: use ``ResidentModel.gated``, which decodes them again.
+    To capture a backward pass into a CUDA graph, capture ``gated_ffn_backward``:
+    autograd's own joins the streams of other graphs of the same leaves that are
+    still alive, which a capture forbids."""
     import torch
     _check_gated(x, w_gate, w_up, act)
     if (x.requires_grad or w_gate.requires_grad or w_up.requires_grad) and torch.is_grad_enabled():
@@ -422,10 +422,10 @@ def linear_cross_entropy(x, w_head, targets, ignore_index: int = -100, reduction
     tokens not ignored (0 if there is none); with ``return_lse`` also the log
     of each token's sum of exponentials (not differentiable).
 
-    Differentiable for x and w_head (once, in reverse mode); the backward pass computes the
-    logits again, a piece of the vocabulary at a time, so w_head must still
-    hold the same values there (``ResidentModel.cross_entropy`` decodes it
-    again). To capture a backward pass into a CUDA graph, capture
+    Differentiable for x and w_head (once, in reverse mode); the backward pass
+    computes the logits again, a piece of the vocabulary at a time, so w_head
+    must still hold the same values there (``ResidentModel.cross_entropy``
+    decodes it again). To capture a backward pass into a CUDA graph, capture
     ``linear_cross_entropy_backward`` (see ``gated_ffn``)."""
     import torch
     _check_xent(x, w_head, targets, reduction)
@@ -626,9 +626,9 @@ class TiledWeights:
     def gated(self, gate: int, up: int, x, act: str = "silu", out=None, stream=None, status=None):
         """h = act(x W_gate^T) * (x W_up^T) for two matrices of one shape, held
         in tile order: both products in one launch where it takes them together
-        (x: M x cols BF16, M <= 256), then the activation and the product. Returns ``out`` (M x rows
-        BF16, allocated if None). Not differentiable (``ResidentModel.gated``
-        is): an x that asks for a gradient is refused."""
+        (x: M x cols BF16, M <= 256), then the activation and the product.
+        Returns ``out`` (M x rows BF16, allocated if None). Not differentiable
+        (``ResidentModel.gated`` is): an x that asks for a gradient is refused."""
         import torch
         act_id = _act_id(act)
         _refuse_tangents(x)
@@ -640,6 +640,8 @@ class TiledWeights:
         if any(x.device != self.blobs[i].device for i in (gate, up)):
             raise ValueError("x must be on the matrices' device")
         M = int(x.shape[0])
+        if out is not None:
+            _check_out(out, (M, rows), x)
         with _On(x.device, stream, (x, out, status)) as s:
             # laid out on the stream that reads it
             x = x.contiguous()
@@ -647,8 +649,6 @@ class TiledWeights:
                 x = x.clone()
             if out is None:
                 out = torch.empty((M, rows), dtype=torch.bfloat16, device=x.device)
-            else:
-                _check_out(out, (M, rows), x)
             ab = torch.empty((2, M, rows), dtype=torch.float32, device=x.device)
             if self._one_launch(gate, up):
                 self.gemm_batched([gate, up], [x, x], [ab[0], ab[1]], stream=s, status=status)
@@ -844,9 +844,11 @@ class ResidentModel:
         rows, BF16), then the activation and the product; "decode": both
         matrices decoded into a temporary buffer, then ``gated_ffn``'s kernel;
         "auto": the faster of the two by codec, rows and columns (the decode
-        route for blobs that the fused layer does not take). Differentiable
-        for x: the backward pass decodes the matrices again instead of keeping
-        them."""
+        route for blobs that the fused layer does not take). The fused DFloat11
+        layer adds parts of a row atomically, so the last bits of its products
+        may vary from run to run; every other route repeats bit for bit.
+        Differentiable for x: the backward pass decodes the matrices again
+        instead of keeping them."""
         import torch
         if route not in ("auto", "fused", "decode"):
             raise ValueError(f"unknown route {route!r}")
